@@ -488,6 +488,114 @@ moe_status moe_block_noalloc(const uint16_t *x, const float *w_router, int32_t t
                              uint32_t *topk_idx, float *topk_w, uint32_t *offsets, uint32_t *csr_rows,
                              float *csr_w, uint32_t *csr_pos, float *out, int32_t accumulate, void *stream);
 
+/*
+ * Layer operators around the block: what a layer runs between its MoE
+ * sub-layers on the same 4-bit weights (prefill.rs page, fn pf_layer: the
+ * fused norm before a sub-layer; experts.rs page, fn pf_experts: the dense
+ * `qmm` projections and silu_mul; prefill.rs page, fn prefill_chunk: the
+ * vocabulary head's qmm).
+ *
+ * Rows are bf16, fp32 or 8-bit: e4m3 codes (OCP: 4 exponent bits, bias 7,
+ * largest finite value 448, 0x7f / 0xff NaN) with scales,
+ *
+ *   MOE_SCALE_NONE   value = code                       (scales ignored)
+ *   MOE_SCALE_ROW    value = code * scale[row]          scale fp32 [t]
+ *   MOE_SCALE_BLOCK  value = code * 2^(scale[row][c/32] - 127)
+ *                    scale u8 [t][width/32], contiguous, no 255
+ *
+ * A matrix of rows has its own row stride (ldx, ldo, ...: elements between
+ * the starts of consecutive rows, at least the row's width), so a slice of a
+ * wider buffer's columns is passed as it is.  Rows that are read, and rows
+ * of moe_residual_norm that are written, start 16-byte aligned (pointer and
+ * stride); outputs of the projections are aligned to their element.  All
+ * three calls are one kernel launch, need no workspace, keep no state and
+ * give bitwise the same results for the same arguments.
+ */
+enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_E4M3 = 2 };
+enum { MOE_SCALE_NONE = 0, MOE_SCALE_ROW = 1, MOE_SCALE_BLOCK = 2 };
+
+/*
+ * Byte layout of one 4-bit matrix [n x k] (rows = outputs): code section and
+ * scale/bias section, with the tiles and entries of an expert record's
+ * matrix (see moe_layout), the rows padded to a multiple of 32 (the padding's
+ * bytes are read but never reach an output).  Sections are 256-byte aligned.
+ * moe_matrix_layout_make fills *out [host] for 1 <= n <= 2^24, k % 64 == 0,
+ * 64 <= k <= 65536, group in {32, 64}; MOE_ERR_INVALID otherwise.  Host only.
+ */
+typedef struct {
+    int32_t n, k, group, reserved;
+    uint64_t w, sb;   /* byte offsets of the codes and of the scale/bias pairs */
+    uint64_t bytes;   /* size of the whole record */
+} moe_matrix_layout;
+moe_status moe_matrix_layout_make(int32_t n, int32_t k, int32_t group, moe_matrix_layout *out);
+
+/*
+ * Rows times a 4-bit matrix:
+ *
+ *   out[r][j] (+)= sum_i W[j][i] * x[r][i],   W = scale * q + bias
+ *
+ *   x          bf16 or e4m3 [t][k] (x_type), row stride ldx; x_scale and
+ *              x_scale_kind for e4m3 (bf16: MOE_SCALE_NONE)
+ *   M          [host] layout; record: M->bytes bytes, 16-byte aligned
+ *   out        bf16 or fp32 [t][n] (out_type), row stride ldo; accumulate = 0
+ *              overwrites, 1 adds (in fp32, one rounding)
+ * Products of codes and rows are summed exactly as they are (no weight is
+ * rounded): per group, scale * sum(q x) + bias * sum(x), every sum in fp32,
+ * so a row's group sums 15 * sum|x| have to stay inside fp32's range.  A row that
+ * holds a NaN or an infinity gives outputs that are not finite; other rows
+ * are not affected.
+ * Requires 1 <= t <= 4096.  out must not overlap x, its scales or the record.
+ */
+moe_status moe_linear(const void *x, int32_t x_type, int64_t ldx, const void *x_scale, int32_t x_scale_kind,
+                      int32_t t, const moe_matrix_layout *M, const void *record, void *out, int32_t out_type,
+                      int64_t ldo, int32_t accumulate, void *stream);
+
+/*
+ * The gated pair of a feed-forward block, both projections, the activation
+ * and the product in one launch:
+ *
+ *   out[r][j] = silu(sum_i Wg[j][i] x[r][i]) * (sum_i Wu[j][i] x[r][i])
+ *
+ * with x as for moe_linear and two records of the layout M.  out is bf16 or
+ * fp32 [t][n], or e4m3 with MOE_SCALE_BLOCK scales out_scale u8 [t][n/32]
+ * (n % 32 == 0), quantised as moe_residual_norm does: the 8-bit rows that
+ * the down projection reads.  out_scale is NULL for the other types.
+ */
+moe_status moe_linear_gated(const void *x, int32_t x_type, int64_t ldx, const void *x_scale, int32_t x_scale_kind,
+                            int32_t t, const moe_matrix_layout *M, const void *gate_record, const void *up_record,
+                            void *out, int32_t out_type, int64_t ldo, uint8_t *out_scale, void *stream);
+
+/*
+ * A sub-layer's output added to the residual stream, and the stream's RMS
+ * norm as bf16 rows, as 8-bit rows, or both:
+ *
+ *   s = x + residual, rounded to the residual's type     -> residual_out
+ *   y = s * gamma / sqrt(mean(s^2) + eps)                -> out (bf16), codes
+ *
+ * The norm is that of the stored (rounded) stream, so it can be recomputed
+ * from it.  8-bit rows: per row scale = max(max|y| / 448, 2^-126); per block
+ * of 32 columns the smallest power of two 2^E, -127 <= E <= 127, with
+ * max|y| <= 448 * 2^E (E = -127 for a block of zeros), stored as E + 127;
+ * codes are y / scale rounded to nearest even, at most +-448.  A y that is
+ * not finite becomes the code NaN and does not count towards the scale.
+ *
+ *   x             bf16 or fp32 [t][h] (x_type), row stride ldx
+ *   residual      bf16 or fp32 [t][h] (res_type), row stride ldr, or NULL: s = x
+ *   residual_out  [t][h] of res_type, row stride ldr, or NULL; may be
+ *                 `residual` itself; NULL if residual is
+ *   gamma         fp32 [h], 16-byte aligned;  eps >= 0, finite
+ *   out           bf16 [t][h], row stride ldo, or NULL
+ *   codes         e4m3 [t][h], row stride ldc, or NULL; scale and scale_kind
+ *                 (MOE_SCALE_ROW or MOE_SCALE_BLOCK) as above
+ * At least one of out and codes.  No output may overlap an input (but for
+ * residual_out) or another output.  Requires 1 <= t <= 4096, h % 32 == 0,
+ * 32 <= h <= 16384.
+ */
+moe_status moe_residual_norm(const void *x, int32_t x_type, int64_t ldx, const void *residual, void *residual_out,
+                             int32_t res_type, int64_t ldr, const float *gamma, float eps, int32_t t, int32_t h,
+                             uint16_t *out, int64_t ldo, uint8_t *codes, int64_t ldc, void *scale,
+                             int32_t scale_kind, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

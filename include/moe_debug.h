@@ -43,9 +43,10 @@ enum {
     MOE_PHASE_GATEUP = 6,      /* routed grouped gate/up + SiLU*up */
     MOE_PHASE_DOWN = 7,        /* routed grouped down */
     MOE_PHASE_COMBINE = 8,     /* weighted combine into out */
-    MOE_PHASE_NORM = 9,        /* injection into the residual copies and the next norm */
+    MOE_PHASE_NORM = 9,        /* injection into the residual copies and the next norm; moe_residual_norm */
     MOE_PHASE_EXPERTS = 10,    /* routed grouped gate/up + SiLU*up and down in one launch */
-    MOE_PHASES = 11
+    MOE_PHASE_LINEAR = 11,     /* moe_linear and moe_linear_gated */
+    MOE_PHASES = 12
 };
 void moe_profile_begin(uint32_t mask);
 int moe_profile_end(double *ms, int64_t *launches);

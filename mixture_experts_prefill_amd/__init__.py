@@ -52,6 +52,11 @@ class moe_next_norm(ctypes.Structure):
                 ("mixed", ctypes.c_void_p)]
 
 
+class moe_matrix_layout(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("w", ctypes.c_uint64), ("sb", ctypes.c_uint64), ("bytes", ctypes.c_uint64)]
+
+
 class moe_ring_stats(ctypes.Structure):
     _fields_ = [("jobs", ctypes.c_int32), ("streamed", ctypes.c_int32), ("batches", ctypes.c_int32),
                 ("fetched_bytes", ctypes.c_uint64), ("wait_ms", ctypes.c_double)]
@@ -64,7 +69,8 @@ EXPORTS = ["moe_last_error", "moe_layout_make", "moe_workspace_bytes", "moe_rout
            "moe_prefill_fused", "moe_block", "moe_block_noalloc", "moe_inject_norm", "moe_block_next_norm",
            "moe_layout_make_bits", "moe_ring_set_miss_layout", "moe_residency", "moe_lookahead",
            "moe_block_from_residual", "moe_chunk_stats_fill", "moe_debug_read_probe",
-           "moe_debug_schedule", "moe_debug_xcc_map", "moe_debug_tile_wait"]
+           "moe_debug_schedule", "moe_debug_xcc_map", "moe_debug_tile_wait", "moe_matrix_layout_make",
+           "moe_linear", "moe_linear_gated", "moe_residual_norm"]
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 PHASES = ["router", "topk", "csr", "shared_gateup", "shared_down", "schedule", "gateup", "down", "combine", "norm",
           "experts"]
@@ -113,6 +119,11 @@ def lib():
     L.moe_lookahead.argtypes = [P, P, I, I, I, I, I, P, P, P, P, P, P, P]
     L.moe_block_from_residual.argtypes = [P, NP, P, I, I, I, LP, P, LP, P, P, P, P, P, P, P, P, P, NP, P, I, P, Z,
                                           P]
+    Q, MP = ctypes.c_int64, ctypes.POINTER(moe_matrix_layout)
+    L.moe_matrix_layout_make.argtypes = [I, I, I, MP]
+    L.moe_linear.argtypes = [P, I, Q, P, I, I, MP, P, P, I, Q, I, P]
+    L.moe_linear_gated.argtypes = [P, I, Q, P, I, I, MP, P, P, P, I, Q, P, P]
+    L.moe_residual_norm.argtypes = [P, I, Q, P, P, I, Q, P, ctypes.c_float, I, I, P, Q, P, Q, P, I, P]
     L.moe_ring_plan_debug.argtypes = [P, P, I, I, I, P, P, P]
     L.moe_profile_begin.argtypes = [ctypes.c_uint32]
     L.moe_profile_begin.restype = None
@@ -122,7 +133,8 @@ def lib():
     L.moe_profile_end.restype = ctypes.c_int
     for f in ("moe_layout_make", "moe_layout_make_bits", "moe_ring_set_miss_layout", "moe_route", "moe_build_csr", "moe_shared", "moe_ring_create",
               "moe_ring_get_stats", "moe_prefill_experts", "moe_prefill_fused", "moe_block", "moe_block_noalloc", "moe_inject_norm", "moe_block_next_norm",
-              "moe_residency", "moe_lookahead", "moe_block_from_residual", "moe_chunk_stats_fill"):
+              "moe_residency", "moe_lookahead", "moe_block_from_residual", "moe_chunk_stats_fill",
+              "moe_matrix_layout_make", "moe_linear", "moe_linear_gated", "moe_residual_norm"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
@@ -419,6 +431,134 @@ def moe_block_from_residual(pending_y: Optional[torch.Tensor], in_norm: moe_next
                                          _stream(stream)))
 
 
+# ------------------------------------------------------------------ layer operators
+# Rows are 2-D tensors whose last dimension is contiguous; the row stride is
+# theirs, so column slices of a wider buffer are passed as they are.
+
+BF16, F32, E4M3 = 0, 1, 2                            # MOE_BF16, MOE_F32, MOE_E4M3
+SCALE_NONE, SCALE_ROW, SCALE_BLOCK = 0, 1, 2         # MOE_SCALE_*
+_ROW_TYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.float8_e4m3fn: E4M3}
+_BLOCK_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _row_args(x: torch.Tensor, t: int, width: int, what: str):
+    """(pointer, type, row stride) of a t x width row tensor."""
+    if x.dim() != 2 or x.shape[0] != t or x.shape[1] != width:
+        raise ValueError(f"{what} must be a [{t}, {width}] tensor, not {list(x.shape)}")
+    kind = _ROW_TYPES.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"{what} must be bfloat16, float32 or float8_e4m3fn, not {x.dtype}")
+    ld, step = x.stride()
+    if (step != 1 and width > 1) or (ld < width and t > 1):
+        raise ValueError(f"{what} needs a contiguous last dimension and rows that do not overlap")
+    return x.data_ptr(), kind, ld if t > 1 and ld >= width else width + -width % 16
+
+
+def _scale_args(scale: Optional[torch.Tensor], t: int, width: int, what: str):
+    """(pointer, kind) of the scales of 8-bit rows."""
+    if scale is None:
+        return None, SCALE_NONE
+    if scale.dtype == torch.float32:
+        kind, n = SCALE_ROW, t
+    elif scale.dtype in _BLOCK_SCALE_TYPES:
+        kind, n = SCALE_BLOCK, t * (width // 32)
+    else:
+        raise ValueError(f"{what} must be float32 (one a row) or uint8 / float8_e8m0fnu (one per 32 columns)")
+    if scale.numel() != n or not scale.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} values")
+    return scale.data_ptr(), kind
+
+
+def _launch_device(*tensors: Optional[torch.Tensor]) -> torch.device:
+    """The one GPU that all the tensors are on."""
+    dev = None
+    for x in tensors:
+        if x is None:
+            continue
+        if not x.is_cuda or (dev is not None and x.device != dev):
+            raise ValueError("tensors passed to libmoe must be on one GPU")
+        dev = x.device
+    return dev
+
+
+def _call_on(dev: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream) with `dev` current, on the given stream or dev's current one."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def moe_matrix_layout_make(n: int, k: int, group: int) -> moe_matrix_layout:
+    out = moe_matrix_layout()
+    _check(lib().moe_matrix_layout_make(n, k, group, ctypes.byref(out)))
+    return out
+
+
+def _check_record(record: torch.Tensor, layout: moe_matrix_layout) -> int:
+    if not record.is_contiguous() or record.numel() * record.element_size() < layout.bytes:
+        raise ValueError(f"a record of this layout is {layout.bytes} contiguous bytes")
+    return record.data_ptr()
+
+
+def moe_linear(x: torch.Tensor, layout: moe_matrix_layout, record: torch.Tensor, out: torch.Tensor,
+               x_scale: Optional[torch.Tensor] = None, accumulate: int = 0, stream=None) -> None:
+    """out [t, n] (bf16 or fp32) (+)= x [t, k] times the 4-bit matrix; x bf16, or
+    e4m3 with x_scale fp32 [t] or uint8 / float8_e8m0fnu [t, k/32]."""
+    dev = _launch_device(x, record, out, x_scale)
+    t = x.shape[0]
+    xp, xt, ldx = _row_args(x, t, layout.k, "x")
+    op, ot, ldo = _row_args(out, t, layout.n, "out")
+    sp, sk = _scale_args(x_scale, t, layout.k, "x_scale")
+    _call_on(dev, stream, lib().moe_linear, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
+             _check_record(record, layout), op, ot, ldo, accumulate)
+
+
+def moe_linear_gated(x: torch.Tensor, layout: moe_matrix_layout, gate_record: torch.Tensor, up_record: torch.Tensor,
+                     out: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
+                     out_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out [t, n] = silu(x Wg^T) * (x Wu^T); out bf16, fp32, or e4m3 with
+    out_scale uint8 / float8_e8m0fnu [t, n/32]; x as for moe_linear."""
+    dev = _launch_device(x, gate_record, up_record, out, x_scale, out_scale)
+    t = x.shape[0]
+    xp, xt, ldx = _row_args(x, t, layout.k, "x")
+    op, ot, ldo = _row_args(out, t, layout.n, "out")
+    sp, sk = _scale_args(x_scale, t, layout.k, "x_scale")
+    qp, qk = _scale_args(out_scale, t, layout.n, "out_scale")
+    if qk == SCALE_ROW:
+        raise ValueError("out_scale is one byte per 32 columns")
+    _call_on(dev, stream, lib().moe_linear_gated, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
+             _check_record(gate_record, layout), _check_record(up_record, layout), op, ot, ldo, qp)
+
+
+def moe_residual_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                      residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """residual_out = x + residual (rounded to its type) and the RMS norm of it
+    as bf16 rows `out`, as e4m3 rows `codes` with `scale` (fp32 [t], or uint8 /
+    float8_e8m0fnu [t, h/32]), or both; without a residual the norm of x."""
+    dev = _launch_device(x, gamma, residual, residual_out, out, codes, scale)
+    t, h = x.shape
+    xp, xt, ldx = _row_args(x, t, h, "x")
+    rp, rt, ldr = (None, BF16, 0) if residual is None else _row_args(residual, t, h, "residual")
+    rop = None
+    if residual_out is not None:
+        rop, rot, ldro = _row_args(residual_out, t, h, "residual_out")
+        if residual is not None and (rot, ldro) != (rt, ldr):
+            raise ValueError("residual_out must have the residual's type and row stride")
+    op, ot, ldo = (None, BF16, 0) if out is None else _row_args(out, t, h, "out")
+    cp, ct, ldc = (None, E4M3, 0) if codes is None else _row_args(codes, t, h, "codes")
+    sp, sk = _scale_args(scale, t, h, "scale")
+    if ot != BF16 or ct != E4M3 or (codes is None) != (scale is None):
+        raise ValueError("out is bfloat16, codes are float8_e4m3fn and have a scale")
+    if gamma.dtype != torch.float32 or gamma.numel() != h or not gamma.is_contiguous():
+        raise ValueError(f"gamma must be contiguous float32 [{h}]")
+    _call_on(dev, stream, lib().moe_residual_norm, xp, xt, ldx, rp, rop, rt, ldr, gamma.data_ptr(), eps, t, h, op, ldo,
+             cp, ldc, sp, sk)
+
+
 def moe_ring_plan_debug(offsets, resident, n_slots: int = 64, group: int = 8):
     """Host-only ring schedule (numpy in, numpy out): slot[E], batch[E], wait[batches]."""
     import numpy as np
@@ -462,3 +602,4 @@ def moe_profile_end() -> dict:
 
 
 from .block import MoeBlock  # noqa: E402  (device-buffer owner built on the calls above)
+from .matrix import MoeMatrix  # noqa: E402

@@ -218,4 +218,33 @@ hipError_t launch_chunk_stats(const uint32_t *offsets, int t, int E, moe_chunk_s
 constexpr int kNormMaxHidden = 16384;
 hipError_t launch_next_norm(const NextNormArgs &a, hipStream_t s);
 
+// Residual addition, RMS norm and 8-bit rows (resnorm.hip); the fields are
+// moe_residual_norm's arguments (scale_kind: MOE_SCALE_ROW or _BLOCK).
+struct ResidualNormArgs {
+    const void *x, *residual;
+    void *residual_out;
+    const float *gamma;
+    uint16_t *out;
+    uint8_t *codes;
+    void *scale;
+    int64_t ldx, ldr, ldo, ldc;
+    int x_type, res_type, scale_kind, t, h;
+    float eps;
+};
+hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t s);
+
+// Rows times one 4-bit matrix, or the gated pair (record2 set) (linear.hip).
+struct LinearArgs {
+    const uint8_t *x;
+    int64_t ldx_bytes;
+    const void *x_scale;
+    const uint8_t *record, *record2;
+    uint64_t w, sb;          // sections of a record
+    void *out;
+    int64_t ldo;
+    uint8_t *out_scale;      // gated with e4m3 output
+    int x_type, x_scale_kind, out_type, accumulate, t, n, k, group;
+};
+hipError_t launch_linear(const LinearArgs &a, hipStream_t s);
+
 }  // namespace moe
