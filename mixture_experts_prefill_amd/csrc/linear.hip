@@ -25,6 +25,8 @@
 // of ones, in the accumulator's layout.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "moe_internal.h"
 #include "quant8.h"
 
@@ -35,6 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 #define GLOBAL __attribute__((address_space(1)))
@@ -47,6 +50,17 @@ __device__ __forceinline__ u32x4 load16_once(const uint8_t *p) {
 }
 __device__ __forceinline__ u32x2 load8(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL u32x2 *>(reinterpret_cast<uintptr_t>(p));
+}
+// A buffer of `bytes` bytes from p on (the same for every lane), and non-temporal loads from it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
+}
+constexpr int kNonTemporal = 2;
+__device__ __forceinline__ u32x2 buffer_load8(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, offset, kNonTemporal));
+}
+__device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
+    return __builtin_amdgcn_raw_buffer_load_b32(b, lane_offset, offset, kNonTemporal);
 }
 __device__ __forceinline__ uint32_t load4_once(const uint8_t *p) {
     return __builtin_nontemporal_load(reinterpret_cast<const GLOBAL uint32_t *>(reinterpret_cast<uintptr_t>(p)));
@@ -65,7 +79,24 @@ __device__ __forceinline__ u32x2 code_bytes(uint32_t w) {
     return (u32x2){__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
 }
 
-// The 8 codes of a word as bf16.
+// The 8 codes of a word as bf16, in the order 0 4 1 5 2 6 3 7 in which the
+// nibbles fall into bytes; the rows' 8 columns are put in the same order
+// (permute8) where that is done once for many words.
+__device__ __forceinline__ bf16x8 code_bf16_as_split(uint32_t w) {
+    const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+    const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+    const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+    const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+    const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    return (bf16x8){v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+}
+// 8 bf16 values 0 .. 7 in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ u32x4 permute8(u32x4 v) {
+    return (u32x4){__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                   __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+}
+
+// The 8 codes of a word as bf16, in order.
 __device__ __forceinline__ bf16x8 code_bf16(uint32_t w) {
     const u32x2 b = code_bytes(w);
     const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b.x, 512.0f, false);
@@ -102,7 +133,7 @@ struct XRaw<MOE_E4M3> {
     uint32_t scale[2];  // of the step's two 32-column blocks
 };
 
-// p: the token's row; scale: its block scales or nullptr.
+// p: the token's row; scale: its block scales (or any bytes that may be read).
 template <int XT, int G>
 __device__ __forceinline__ XRaw<XT> load_x(const uint8_t *p, int kb, int half, const uint8_t *scale) {
     XRaw<XT> f;
@@ -121,15 +152,8 @@ __device__ __forceinline__ XRaw<XT> load_x(const uint8_t *p, int kb, int half, c
 #pragma unroll
             for (int i = 0; i < 4; ++i) f.v[i] = load8(p + piece_column<G>(i, half));
         }
-        f.scale[0] = f.scale[1] = 127;
-        if (scale) {
-            if (G == 64) {
-                f.scale[0] = load1(scale + kb * 2 + half);
-            } else {
-                f.scale[0] = load1(scale + kb * 2);
-                f.scale[1] = load1(scale + kb * 2 + 1);
-            }
-        }
+        f.scale[0] = load1(scale + kb * 2 + (G == 64 ? half : 0));
+        f.scale[1] = G == 64 ? 0 : load1(scale + kb * 2 + 1);
     }
     return f;
 }
@@ -148,12 +172,12 @@ struct Frag {
     bf16x8 v[4];
 };
 template <int XT, int G>
-__device__ __forceinline__ Frag x_frag(const XRaw<XT> &x) {
+__device__ __forceinline__ Frag x_frag(const XRaw<XT> &x, bool block_scales) {
     Frag f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (XT == MOE_BF16) f.v[i] = __builtin_bit_cast(bf16x8, x.v[i]);
-        else f.v[i] = e4m3_bf16(x.v[i], __uint_as_float(x.scale[G == 64 ? 0 : i & 1] << 23));
+        else f.v[i] = e4m3_bf16(x.v[i], __uint_as_float((block_scales ? x.scale[G == 64 ? 0 : i & 1] : 127u) << 23));
     }
     return f;
 }
@@ -198,33 +222,17 @@ __device__ __forceinline__ f32x16 group_sum(const Frag &x, int gi) {
 
 // ---------------------------------------------------------------- epilogue
 
-// One finished output value (the pair g, u when gated).  All 64 lanes of the
-// wave call it together: the 32 lanes of a half hold 32 adjacent outputs of
-// one row, the block of an 8-bit output's scale.
+// An fp16 scale or bias in a register of its own.  Left to itself the compiler
+// widens it inside every multiply-add (v_fma_mix_f32), at half the rate.
+__device__ __forceinline__ float in_f32(_Float16 h) {
+    float f = (float)h;
+    asm("" : "+v"(f));
+    return f;
+}
+
+// One output value of live row and column (no 8-bit type).
 template <bool GATED>
-__device__ __forceinline__ void store_out(const LinearArgs &a, int row, int col, float v, float u) {
-    const bool live = row < a.t && col < a.n;
-    if (a.x_scale_kind == MOE_SCALE_ROW) {
-        const float s = static_cast<const float *>(a.x_scale)[min(row, a.t - 1)];
-        v *= s;
-        u *= s;
-    }
-    if (GATED) {
-        v = silu_mul(v, u);
-        if (a.out_type == MOE_E4M3) {
-            float m = q8::magnitude(v);
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-            const uint32_t byte = q8::block_byte(m);
-            const uint32_t code = q8::finite(v) ? q8::codes2(v * q8::block_inverse(byte), 0.0f) & 0xffu : q8::kNaN;
-            if (live) {
-                static_cast<uint8_t *>(a.out)[(size_t)row * a.ldo + col] = (uint8_t)code;
-                if ((col & 31) == 0) a.out_scale[(size_t)row * (a.n / 32) + col / 32] = (uint8_t)byte;
-            }
-            return;
-        }
-    }
-    if (!live) return;
+__device__ __forceinline__ void store_one(const LinearArgs &a, int row, int col, float v) {
     if (a.out_type == MOE_F32) {
         float *p = static_cast<float *>(a.out) + (size_t)row * a.ldo + col;
         *p = (!GATED && a.accumulate) ? *p + v : v;
@@ -234,12 +242,51 @@ __device__ __forceinline__ void store_out(const LinearArgs &a, int row, int col,
     }
 }
 
+// RH finished outputs of one row, columns col + (32 / RH) i (gated: then the
+// RH of the second matrix).  All lanes of a wave call it together; the 32 / RH
+// lanes of one row are adjacent, and together they hold 32 adjacent outputs,
+// the block of an 8-bit output's scale.
+template <bool GATED, int RH, int SPAN = 32 / RH>
+__device__ __forceinline__ void store_units(const LinearArgs &a, int row, int col, float *v) {
+    const bool live = row < a.t;
+    if (a.x_scale_kind == MOE_SCALE_ROW) {
+        const float s = static_cast<const float *>(a.x_scale)[min(row, a.t - 1)];
+#pragma unroll
+        for (int i = 0; i < (GATED ? 2 : 1) * RH; ++i) v[i] *= s;
+    }
+    if (GATED) {
+#pragma unroll
+        for (int i = 0; i < RH; ++i) v[i] = silu_mul(v[i], v[RH + i]);
+        if (a.out_type == MOE_E4M3) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < RH; ++i) m = fmaxf(m, q8::magnitude(v[i]));
+#pragma unroll
+            for (int off = SPAN / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+            const uint32_t byte = q8::block_byte(m);
+#pragma unroll
+            for (int i = 0; i < RH; ++i) {
+                const int c = col + SPAN * i;
+                const uint32_t code = q8::finite(v[i]) ? q8::codes2(v[i] * q8::block_inverse(byte), 0.0f) & 0xffu : q8::kNaN;
+                if (live && c < a.n) static_cast<uint8_t *>(a.out)[(size_t)row * a.ldo + c] = (uint8_t)code;
+            }
+            if (live && (col & 31) == 0 && col < a.n) a.out_scale[(size_t)row * (a.n / 32) + col / 32] = (uint8_t)byte;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RH; ++i)
+        if (live && col + SPAN * i < a.n) store_one<GATED>(a, row, col + SPAN * i, v[i]);
+}
+
 // ---------------------------------------------------------------- few rows
 
 // A workgroup computes 32 outputs (of both matrices when gated) for 32 MT
 // rows; its W waves split the 64-column steps (wave w takes steps w, w + W,
 // ...) and their sums meet in LDS, added in wave order.  U steps' loads are
-// issued before the first is used.  NR: accumulator registers that hold live
+// issued before the first is used; steps past the last repeat it with scale
+// and bias 0 (a branch around them made the compiler move the loads to their
+// use, one memory latency after another).  NR: accumulator registers that hold live
 // rows (4 for up to 8 rows, 8 for 16, else 16).  Rows past the last load the
 // last row's values and store nothing.
 template <int XT, int G, bool GATED, int MT, int NR, int W, int U>
@@ -252,14 +299,14 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
     const int ob = blockIdx.x, t0 = blockIdx.y * 32 * MT;
     const int nkb = a.k >> 6;
 
+    const bool block_scales = a.x_scale_kind == MOE_SCALE_BLOCK;
     const uint8_t *xp[MT], *xs[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int r = min(t0 + 32 * m + row, a.t - 1);
         xp[m] = a.x + (size_t)r * a.ldx_bytes;
-        xs[m] = a.x_scale_kind == MOE_SCALE_BLOCK
-                    ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5)
-                    : nullptr;
+        // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
+        xs[m] = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : xp[m];
     }
     const uint8_t *wp[NW], *sp[NW];
 #pragma unroll
@@ -290,23 +337,24 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) xv[u][m] = load_x<XT, G>(xp[m], kb, half, xs[m]);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (k0 + u * W >= nkb) break;
+            const uint32_t live = k0 + u * W < nkb ? ~0u : 0u;
             Frag wf[NW];
 #pragma unroll
             for (int f = 0; f < NW; ++f) wf[f] = w_frag<G>(wv[u][f]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const Frag xf = x_frag<XT, G>(xv[u][m]);
+                const Frag xf = x_frag<XT, G>(xv[u][m], block_scales);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const f32x16 xsum = group_sum<G>(xf, g);
 #pragma unroll
                     for (int f = 0; f < NW; ++f) {
                         const f32x16 d = group_product<G>(xf, wf[f], g);
-                        const half2_t sb = __builtin_bit_cast(half2_t, sv[u][f][g]);
-                        const float s = (float)sb.x, b = (float)sb.y;
+                        const half2_t sb = __builtin_bit_cast(half2_t, sv[u][f][g] & live);
+                        const float s = in_f32(sb.x), b = in_f32(sb.y);
 #pragma unroll
                         for (int r = 0; r < NR; ++r)
                             acc[f][m][r] = __builtin_fmaf(b, xsum[r], __builtin_fmaf(s, d[r], acc[f][m][r]));
@@ -332,24 +380,329 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
 #pragma unroll
                 for (int w = 1; w < W; ++w) v[f] += red[w][f][r][lane];
             }
-            store_out<GATED>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), ob * 32 + row, v[0], v[NW - 1]);
+            store_units<GATED, 1>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), ob * 32 + row, v);
         }
     }
 }
 
+// ---------------------------------------------------------------- up to 64 rows
+
+// Bound by the weights' bytes: every code is read once, by one wave, and all
+// else is arranged so that enough loads are in flight and few instructions are
+// spent on a code.  The matrix core runs 16x16x32 products (tokens x outputs;
+// a 16-token block costs a quarter of the 32x32 form's time when there are few
+// tokens).  A unit is 16 outputs; a wave owns RH units (of both matrices when
+// gated) for 16 MT rows, and the workgroup's waves split the 64-column steps
+// as above, their sums meeting in LDS in wave order.  The host picks the
+// number of waves (launch_units).
+//
+// Lane (row or output L % 16, quarter L / 16) of a step: with groups of 64,
+// MFMA i takes columns 16 (L / 16) + 8 i of the 64; with groups of 32, MFMA i
+// takes group i's columns 32 i + 8 (L / 16).  Register r of the accumulator's
+// quarter q is operand row 4 q + r; with up to 4 NR rows, NR < 4, the rows are
+// dealt out so that registers 0 .. NR - 1 hold them all and the others, copies,
+// are not scaled and added up at all.
+constexpr int kMaxWaves = 8;
+template <int XT, int G>
+struct URows {
+    u32x4 v[XT == MOE_BF16 ? 2 : 1];  // e4m3: MFMA 0's 8 codes, then MFMA 1's
+    uint32_t scale[2];
+};
+template <int XT, int G>
+__device__ __forceinline__ URows<XT, G> load_unit_rows(const uint8_t *p, int kb, int q, const uint8_t *scale) {
+    URows<XT, G> f;
+    if constexpr (XT == MOE_BF16) {
+        p += kb * 128 + q * (G == 64 ? 32 : 16);
+        f.v[0] = load16(p);
+        f.v[1] = load16(p + (G == 64 ? 16 : 64));
+        f.scale[0] = f.scale[1] = 0;
+    } else {
+        p += kb * 64 + q * (G == 64 ? 16 : 8);
+        if constexpr (G == 64) {
+            f.v[0] = load16(p);
+        } else {
+            const u32x2 a = load8(p), b = load8(p + 32);
+            f.v[0] = (u32x4){a.x, a.y, b.x, b.y};
+        }
+        f.scale[0] = load1(scale + kb * 2 + (G == 64 ? q >> 1 : 0));
+        f.scale[1] = G == 64 ? 0 : load1(scale + kb * 2 + 1);
+    }
+    return f;
+}
+struct UFrag {
+    bf16x8 v[2];
+};
+template <int XT, int G>
+__device__ __forceinline__ UFrag unit_rows(const URows<XT, G> &x, bool block_scales) {
+    UFrag f;
+    if constexpr (XT == MOE_BF16) {
+        f.v[0] = __builtin_bit_cast(bf16x8, x.v[0]);
+        f.v[1] = __builtin_bit_cast(bf16x8, x.v[1]);
+    } else {
+        const float s0 = __uint_as_float((block_scales ? x.scale[0] : 127u) << 23);
+        const float s1 = G == 64 ? s0 : __uint_as_float((block_scales ? x.scale[1] : 127u) << 23);
+        f.v[0] = e4m3_bf16((u32x2){x.v[0].x, x.v[0].y}, s0);
+        f.v[1] = e4m3_bf16((u32x2){x.v[0].z, x.v[0].w}, s1);
+    }
+    return f;
+}
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+//
+// STAGED: the workgroup first copies its rows to LDS, as bf16, with their
+// group sums.  Loaded from the cache for every step instead, they cost as much
+// of its bandwidth as the codes (a lane needs 32 bytes of rows for 16 of codes
+// a step, and most lanes' are copies): 100003 x 2048, one row, 25.7 -> 21 us.
+template <int XT, int G, bool GATED, int MT, int NR, int RH, bool STAGED>
+__global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
+    constexpr int NM = GATED ? 2 : 1, NU = NM * RH, NG = 64 / G;
+    constexpr int U = MT == 1 && NU == 1 ? 4 : MT <= 2 ? 2 : 1;
+    static_assert(MT == 1 || NR == 4, "several row blocks use every register");
+    static_assert(!STAGED || MT == 1, "one row block is staged");
+    extern __shared__ float red[];  // [waves][NU][NR][64]; then the staged sums [K / G][4 NR] and rows
+    const int lane = threadIdx.x & 63, q = lane >> 4, row = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int unit0 = blockIdx.x * RH, t0 = blockIdx.y * 16 * MT;
+    const int nkb = a.k >> 6;
+    const bool block_scales = a.x_scale_kind == MOE_SCALE_BLOCK;
+
+    const uint8_t *xp[MT], *xs[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int r = min(t0 + 16 * m + NR * (row >> 2) + min(row & 3, NR - 1), a.t - 1);
+        xp[m] = a.x + (size_t)r * a.ldx_bytes;
+        // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
+        xs[m] = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : xp[m];
+    }
+    // Staged rows: 16 bytes of padding shift neighbouring rows' LDS banks.
+    const uint32_t stride = a.k * 2 + 16;
+    float *sums = red + (W > 1 ? W * NU * NR * 64 : 0);
+    uint8_t *staged_base = reinterpret_cast<uint8_t *>(sums + nkb * NG * 4 * NR);
+    const uint8_t *staged = staged_base + min(NR * (row >> 2) + min(row & 3, NR - 1), a.t - 1 - t0) * stride;
+    // Buffers over the code and scale sections of the units' tile row (a pair
+    // is one tile; rows are padded to whole tiles): a load is then one scalar
+    // offset a step and one lane offset, without 64-bit lane arithmetic.
+    __amdgpu_buffer_rsrc_t wb[NM], sb[NM];
+    uint32_t wo[RH], so[RH];
+#pragma unroll
+    for (int f = 0; f < NM; ++f) {
+        const uint8_t *rec = f ? a.record2 : a.record;
+        wb[f] = buffer(rec + a.w + (size_t)(unit0 >> 1) * nkb * 1024, nkb * 1024);
+        sb[f] = buffer(rec + a.sb + (size_t)(unit0 >> 1) * nkb * (128 * NG), nkb * (128 * NG));
+    }
+#pragma unroll
+    for (int u = 0; u < RH; ++u) {
+        const int r = 16 * ((unit0 + u) & 1) + row;
+        wo[u] = G == 64 ? (q >> 1) * 512 + r * 16 + (q & 1) * 8 : r * 16 + q * 4;
+        so[u] = r * 4;
+    }
+
+    struct Batch {
+        u32x2 w[U][NU];
+        uint32_t sb[U][NU][NG];
+        URows<XT, G> x[STAGED ? 1 : U][MT];
+    };
+    auto load = [&](Batch &b, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = min(k0 + u * W, nkb - 1);
+#pragma unroll
+            for (int f = 0; f < NU; ++f) {
+                if constexpr (G == 64) b.w[u][f] = buffer_load8(wb[f / RH], wo[f % RH], kb * 1024);
+                else b.w[u][f] = (u32x2){buffer_load4(wb[f / RH], wo[f % RH], kb * 1024), buffer_load4(wb[f / RH], wo[f % RH] + 512, kb * 1024)};
+#pragma unroll
+                for (int g = 0; g < NG; ++g) b.sb[u][f][g] = buffer_load4(sb[f / RH], so[f % RH] + g * 128, kb * (128 * NG));
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                if (!STAGED) b.x[u][m] = load_unit_rows<XT, G>(xp[m], kb, q, xs[m]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    float acc[NU][MT][NR];
+#pragma unroll
+    for (int f = 0; f < NU; ++f)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) acc[f][m][r] = 0.0f;
+    // Steps past the last (in the last batch) repeat it with scale and bias 0.
+    auto compute = [&](const Batch &b, int k0, auto last) {
+        const __bf16 o = (__bf16)1.0f;
+        const bf16x8 one = {o, o, o, o, o, o, o, o};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t live = !decltype(last)::value || k0 + u * W < nkb ? ~0u : 0u;
+            UFrag x[MT];
+            f32x4 xsum[MT][NG];
+            if constexpr (STAGED) {
+                const int kb = min(k0 + u * W, nkb - 1);
+                const uint8_t *p = staged + (uint32_t)kb * 128 + q * (G == 64 ? 32 : 16);
+                x[0].v[0] = *reinterpret_cast<const bf16x8 *>(p);
+                x[0].v[1] = *reinterpret_cast<const bf16x8 *>(p + (G == 64 ? 16 : 64));
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) xsum[0][g][r] = sums[(kb * NG + g) * (4 * NR) + NR * q + r];
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (STAGED) break;
+                x[m] = unit_rows<XT, G>(b.x[u][m], block_scales);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    xsum[m][g] = mfma16(x[m].v[g], one, (f32x4){});
+                    if (G == 64) xsum[m][g] = mfma16(x[m].v[1], one, xsum[m][g]);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < NU; ++f) {
+                const bf16x8 w0 = STAGED ? code_bf16_as_split(b.w[u][f].x) : code_bf16(b.w[u][f].x);
+                const bf16x8 w1 = STAGED ? code_bf16_as_split(b.w[u][f].y) : code_bf16(b.w[u][f].y);
+                float s[NG], c[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const half2_t sb = __builtin_bit_cast(half2_t, b.sb[u][f][g] & live);
+                    // one use each with one register: a mixed multiply-add is the cheaper widening there
+                    s[g] = NR == 1 ? (float)sb.x : in_f32(sb.x);
+                    c[g] = NR == 1 ? (float)sb.y : in_f32(sb.y);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        f32x4 d = mfma16(x[m].v[g], g ? w1 : w0, (f32x4){});
+                        if (G == 64) d = mfma16(x[m].v[1], w1, d);
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+                            acc[f][m][r] = __builtin_fmaf(c[g], xsum[m][g][r], __builtin_fmaf(s[g], d[r], acc[f][m][r]));
+                    }
+            }
+        }
+    };
+
+    Batch b0, b1;
+    int k0 = wave;
+    load(b0, k0);  // in bounds for a wave without a step too
+    if constexpr (STAGED) {
+        const int pieces = a.k >> 3, rows = min(a.t - t0, 4 * NR);
+        for (int r = 0; r < rows; ++r) {
+            const uint8_t *src = a.x + (size_t)(t0 + r) * a.ldx_bytes;
+            const uint8_t *sc = static_cast<const uint8_t *>(a.x_scale) + (size_t)(t0 + r) * (a.k >> 5);
+            for (int c = threadIdx.x; c < pieces; c += blockDim.x) {
+                u32x4 v;
+                if constexpr (XT == MOE_BF16) {
+                    v = load16(src + c * 16);
+                } else {
+                    const uint32_t scale = block_scales ? load1(sc + (c >> 2)) : 127u;
+                    v = __builtin_bit_cast(u32x4, e4m3_bf16(load8(src + c * 8), __uint_as_float(scale << 23)));
+                }
+                *reinterpret_cast<u32x4 *>(staged_base + r * stride + c * 16) = permute8(v);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xffff0000u);
+#pragma unroll
+                for (int off = 1; off < G / 8; off *= 2) sum += __shfl_xor(sum, off, 64);
+                if (c % (G / 8) == 0) sums[(c / (G / 8)) * (4 * NR) + r] = sum;
+            }
+        }
+        // rows past the last: no garbage in the sums (their outputs are not stored)
+        for (int i = threadIdx.x; i < (nkb * NG) * (4 * NR); i += blockDim.x)
+            if (i % (4 * NR) >= rows) sums[i] = 0.0f;
+        __syncthreads();
+    }
+    if (wave < nkb) {
+        while (true) {
+            if (k0 + W * U >= nkb) { compute(b0, k0, std::true_type{}); break; }
+            load(b1, k0 + W * U);
+            compute(b0, k0, std::false_type{});
+            k0 += W * U;
+            if (k0 + W * U >= nkb) { compute(b1, k0, std::true_type{}); break; }
+            load(b0, k0 + W * U);
+            compute(b1, k0, std::false_type{});
+            k0 += W * U;
+        }
+    }
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (W > 1) {
+            if (m) __syncthreads();
+#pragma unroll
+            for (int f = 0; f < NU; ++f)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) red[((wave * NU + f) * NR + r) * 64 + lane] = acc[f][m][r];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (r % W != wave) continue;
+            float v[NU];
+#pragma unroll
+            for (int f = 0; f < NU; ++f) {
+                v[f] = acc[f][m][r];
+                if (W > 1) {
+                    // all reads at once: one LDS latency, not one a wave
+                    float part[kMaxWaves];
+#pragma unroll
+                    for (int w = 0; w < kMaxWaves; ++w) part[w] = red[((min(w, W - 1) * NU + f) * NR + r) * 64 + lane];
+                    v[f] = part[0];
+#pragma unroll
+                    for (int w = 1; w < kMaxWaves; ++w)
+                        v[f] += __uint_as_float(__float_as_uint(part[w]) & (w < W ? ~0u : 0u));
+                }
+            }
+            store_units<GATED, RH, 16>(a, t0 + 16 * m + NR * q + r, unit0 * 16 + row, v);
+        }
+    }
+}
+
+// How k_linear_units runs a call: 16 outputs a wave unless that leaves more
+// than `kUnitWaves` waves even with one wave to a unit pair (or an 8-bit
+// output's block needs two units), and as many waves to split K as bring the
+// launch to about kUnitWaves.
+constexpr int kUnitWaves = 8192;
+constexpr size_t kStagedBytes = 64 * 1024;  // most LDS with staged rows
+
+template <int XT, int G, bool GATED, int MT, int NR>
+hipError_t launch_units_mt(const LinearArgs &a, hipStream_t s) {
+    const int units = (a.n + 15) / 16, nkb = a.k >> 6;
+    const bool pair = (GATED && a.out_type == MOE_E4M3) || units >= 1024 || (units > 256 && a.t > 4);
+    const int wgs = pair ? (units + 1) / 2 : units;
+    const int most = kMaxWaves;
+    int W = 1;
+    while (W < most && W * 2 <= nkb && wgs * W < kUnitWaves) W *= 2;
+    const dim3 grid(wgs, (a.t + 16 * MT - 1) / (16 * MT)), block(64 * W);
+    const int NU = (GATED ? 2 : 1) * (pair ? 2 : 1);
+    const size_t lds = W > 1 ? (size_t)W * NU * NR * 64 * 4 : 0;
+    if constexpr (MT == 1) {
+        const size_t staged = (size_t)(a.k / G) * 4 * NR * 4 + (size_t)a.t * (a.k * 2 + 16);
+        if (lds + staged <= kStagedBytes) {
+            if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 2, true>), grid, block, lds + staged, s, a);
+            else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 1, true>), grid, block, lds + staged, s, a);
+            return hipGetLastError();
+        }
+    }
+    if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 2, false>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 1, false>), grid, block, lds, s, a);
+    return hipGetLastError();
+}
+template <int XT, int G, bool GATED>
+hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
+    if (a.t <= 4) return launch_units_mt<XT, G, GATED, 1, 1>(a, s);
+    if (a.t <= 8) return launch_units_mt<XT, G, GATED, 1, 2>(a, s);
+    if (a.t <= 16) return launch_units_mt<XT, G, GATED, 1, 4>(a, s);
+    if (a.t <= 32) return launch_units_mt<XT, G, GATED, 2, 4>(a, s);
+    return launch_units_mt<XT, G, GATED, 4, 4>(a, s);
+}
+
 template <int XT, int G, bool GATED>
 hipError_t launch_few(const LinearArgs &a, hipStream_t s) {
+    if (a.t <= 64) return launch_units<XT, G, GATED>(a, s);
     const unsigned obs = (unsigned)((a.n + 31) / 32);
-    if (a.t <= 8)
-        hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 1, 4, 8, 4>), dim3(obs), dim3(512), 0, s, a);
-    else if (a.t <= 16)
-        hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 1, 8, 8, 4>), dim3(obs), dim3(512), 0, s, a);
-    else if (a.t <= 32)
-        hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 1, 16, 8, 2>), dim3(obs), dim3(512), 0, s, a);
-    else if (a.t <= 64)
-        hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 2, 16, 8, 1>), dim3(obs), dim3(512), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 4, 16, 4, 1>), dim3(obs, (a.t + 127) / 128), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 4, 16, 4, 1>), dim3(obs, (a.t + 127) / 128), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
