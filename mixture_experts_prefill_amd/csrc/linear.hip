@@ -27,11 +27,14 @@
 
 #include <type_traits>
 
+#include "lds_dma.h"
 #include "moe_internal.h"
 #include "quant8.h"
 
 namespace moe {
 namespace {
+
+using namespace lds;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -56,6 +59,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, int b
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
 }
 constexpr int kNonTemporal = 2;
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_offset, offset, 0));
+}
 __device__ __forceinline__ u32x2 buffer_load8(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, offset, kNonTemporal));
 }
@@ -106,6 +112,11 @@ __device__ __forceinline__ bf16x8 code_bf16(uint32_t w) {
     return (bf16x8){v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
 }
 
+// v + the two bf16 values of a register.
+__device__ __forceinline__ float add_pair(uint32_t u, float v) {
+    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u), one, v, false);
+}
 __device__ __forceinline__ f32x16 mfma_bf16(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -230,6 +241,19 @@ __device__ __forceinline__ float in_f32(_Float16 h) {
     return f;
 }
 
+// The sum of the waves' parts of one value, `stride` floats apart in LDS, in
+// wave order.  All reads go out at once: one LDS latency, not one a wave.
+constexpr int kMaxWaves = 8;
+__device__ __forceinline__ float sum_waves(const float *p, int stride, int W) {
+    float part[kMaxWaves];
+#pragma unroll
+    for (int w = 0; w < kMaxWaves; ++w) part[w] = p[min(w, W - 1) * stride];
+    float v = part[0];
+#pragma unroll
+    for (int w = 1; w < kMaxWaves; ++w) v += __uint_as_float(__float_as_uint(part[w]) & (w < W ? ~0u : 0u));
+    return v;
+}
+
 // One output value of live row and column (no 8-bit type).
 template <bool GATED>
 __device__ __forceinline__ void store_one(const LinearArgs &a, int row, int col, float v) {
@@ -279,24 +303,24 @@ __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int co
         if (live && col + SPAN * i < a.n) store_one<GATED>(a, row, col + SPAN * i, v[i]);
 }
 
-// ---------------------------------------------------------------- few rows
+// ---------------------------------------------------------------- some hundred rows
 
-// A workgroup computes 32 outputs (of both matrices when gated) for 32 MT
-// rows; its W waves split the 64-column steps (wave w takes steps w, w + W,
-// ...) and their sums meet in LDS, added in wave order.  U steps' loads are
-// issued before the first is used; steps past the last repeat it with scale
-// and bias 0 (a branch around them made the compiler move the loads to their
-// use, one memory latency after another).  NR: accumulator registers that hold live
-// rows (4 for up to 8 rows, 8 for 16, else 16).  Rows past the last load the
-// last row's values and store nothing.
-template <int XT, int G, bool GATED, int MT, int NR, int W, int U>
-__global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
-    static_assert(MT == 1 || NR == 16, "several row blocks use every register");
-    constexpr int NW = GATED ? 2 : 1, NG = 64 / G;
-    __shared__ float red[W][NW][NR][64];
+// Too few output tiles to fill the chip with long-running workgroups, so the
+// waves of a workgroup split the 64-column steps (wave w takes steps w, w + W,
+// ...) of one output block, 32 MT rows by NT tiles of 32 outputs (gated: one
+// tile of each matrix), and their sums meet in LDS, added in wave order.  A
+// wave reads its rows and codes straight from the cache into registers, the
+// next step's while this one computes.  Rows past the last load the last
+// row's values and store nothing; steps past the last repeat it with scale and
+// bias 0.
+template <int XT, int G, bool GATED, int MT, int NT>
+__global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
+    static_assert(!GATED || NT == 1, "a gated workgroup has one tile of each matrix");
+    constexpr int NM = GATED ? 2 : 1, NW = NM * NT, NG = 64 / G;
+    extern __shared__ float red[];  // [waves][NW][16][64]
     const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ob = blockIdx.x, t0 = blockIdx.y * 32 * MT;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int ob = blockIdx.x * NT, t0 = blockIdx.y * 32 * MT;
     const int nkb = a.k >> 6;
 
     const bool block_scales = a.x_scale_kind == MOE_SCALE_BLOCK;
@@ -308,59 +332,73 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
         // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
         xs[m] = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : xp[m];
     }
-    const uint8_t *wp[NW], *sp[NW];
+    // a second tile past the matrix is outside the buffer: its codes and scales read as 0
+    const int tiles = min(NT, ((a.n + 31) >> 5) - ob) * nkb;
+    __amdgpu_buffer_rsrc_t wb[NM], sb[NM];
 #pragma unroll
-    for (int f = 0; f < NW; ++f) {
+    for (int f = 0; f < NM; ++f) {
         const uint8_t *rec = f ? a.record2 : a.record;
-        wp[f] = rec + a.w + (size_t)ob * nkb * 1024 + lane * 16;
-        sp[f] = rec + a.sb + (size_t)ob * nkb * (128 * NG) + row * 4;
+        wb[f] = buffer(rec + a.w + (size_t)ob * nkb * 1024, tiles * 1024);
+        sb[f] = buffer(rec + a.sb + (size_t)ob * nkb * (128 * NG), tiles * (128 * NG));
     }
+    struct Batch {
+        u32x4 w[NW];
+        uint32_t sb[NW][NG];
+        XRaw<XT> x[MT];
+    };
+    auto load = [&](Batch &b, int k0) {
+        const int kb = min(k0, nkb - 1);
+#pragma unroll
+        for (int f = 0; f < NW; ++f) {
+            const int at = kb + (f % NT) * nkb;
+            b.w[f] = buffer_load16(wb[f / NT], lane * 16, at * 1024);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) b.sb[f][g] = buffer_load4(sb[f / NT], row * 4 + g * 128, at * (128 * NG));
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) b.x[m] = load_x<XT, G>(xp[m], kb, half, xs[m]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     f32x16 acc[NW][MT];
 #pragma unroll
     for (int f = 0; f < NW; ++f)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[f][m] = (f32x16){};
-
-    for (int k0 = wave; k0 < nkb; k0 += W * U) {
-        u32x4 wv[U][NW];
-        uint32_t sv[U][NW][NG];
-        XRaw<XT> xv[U][MT];
+    auto compute = [&](const Batch &b) {
+        Frag wf[NW];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kb = min(k0 + u * W, nkb - 1);
+        for (int f = 0; f < NW; ++f) wf[f] = w_frag<G>(b.w[f]);
 #pragma unroll
-            for (int f = 0; f < NW; ++f) {
-                wv[u][f] = load16_once(wp[f] + (size_t)kb * 1024);
+        for (int m = 0; m < MT; ++m) {
+            const Frag xf = x_frag<XT, G>(b.x[m], block_scales);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) sv[u][f][g] = load4_once(sp[f] + (size_t)kb * (128 * NG) + g * 128);
-            }
+            for (int g = 0; g < NG; ++g) {
+                const f32x16 xsum = group_sum<G>(xf, g);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) xv[u][m] = load_x<XT, G>(xp[m], kb, half, xs[m]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+                for (int f = 0; f < NW; ++f) {
+                    const f32x16 d = group_product<G>(xf, wf[f], g);
+                    const half2_t h = __builtin_bit_cast(half2_t, b.sb[f][g]);
+                    const float s = in_f32(h.x), c = in_f32(h.y);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t live = k0 + u * W < nkb ? ~0u : 0u;
-            Frag wf[NW];
-#pragma unroll
-            for (int f = 0; f < NW; ++f) wf[f] = w_frag<G>(wv[u][f]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const Frag xf = x_frag<XT, G>(xv[u][m], block_scales);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const f32x16 xsum = group_sum<G>(xf, g);
-#pragma unroll
-                    for (int f = 0; f < NW; ++f) {
-                        const f32x16 d = group_product<G>(xf, wf[f], g);
-                        const half2_t sb = __builtin_bit_cast(half2_t, sv[u][f][g] & live);
-                        const float s = in_f32(sb.x), b = in_f32(sb.y);
-#pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            acc[f][m][r] = __builtin_fmaf(b, xsum[r], __builtin_fmaf(s, d[r], acc[f][m][r]));
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        acc[f][m][r] = __builtin_fmaf(c, xsum[r], __builtin_fmaf(s, d[r], acc[f][m][r]));
                 }
             }
+        }
+    };
+    if (wave < nkb) {
+        Batch b0, b1;
+        int kb = wave;
+        load(b0, kb);
+        while (true) {
+            if (kb + W >= nkb) { compute(b0); break; }
+            load(b1, kb + W);
+            compute(b0);
+            kb += W;
+            if (kb + W >= nkb) { compute(b1); break; }
+            load(b0, kb + W);
+            compute(b1);
+            kb += W;
         }
     }
 
@@ -370,17 +408,13 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
 #pragma unroll
         for (int f = 0; f < NW; ++f)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) red[wave][f][r][lane] = acc[f][m][r];
+            for (int r = 0; r < 16; ++r) red[((wave * NW + f) * 16 + r) * 64 + lane] = acc[f][m][r];
         __syncthreads();
-        for (int r = wave; r < NR; r += W) {
+        for (int r = wave; r < 16; r += W) {
             float v[NW];
 #pragma unroll
-            for (int f = 0; f < NW; ++f) {
-                v[f] = red[0][f][r][lane];
-#pragma unroll
-                for (int w = 1; w < W; ++w) v[f] += red[w][f][r][lane];
-            }
-            store_units<GATED, 1>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), ob * 32 + row, v);
+            for (int f = 0; f < NW; ++f) v[f] = sum_waves(red + (f * 16 + r) * 64 + lane, NW * 16 * 64, W);
+            store_units<GATED, NT, 32>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), ob * 32 + row, v);
         }
     }
 }
@@ -402,7 +436,6 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinearArgs a) {
 // quarter q is operand row 4 q + r; with up to 4 NR rows, NR < 4, the rows are
 // dealt out so that registers 0 .. NR - 1 hold them all and the others, copies,
 // are not scaled and added up at all.
-constexpr int kMaxWaves = 8;
 template <int XT, int G>
 struct URows {
     u32x4 v[XT == MOE_BF16 ? 2 : 1];  // e4m3: MFMA 0's 8 codes, then MFMA 1's
@@ -644,14 +677,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
             for (int f = 0; f < NU; ++f) {
                 v[f] = acc[f][m][r];
                 if (W > 1) {
-                    // all reads at once: one LDS latency, not one a wave
-                    float part[kMaxWaves];
-#pragma unroll
-                    for (int w = 0; w < kMaxWaves; ++w) part[w] = red[((min(w, W - 1) * NU + f) * NR + r) * 64 + lane];
-                    v[f] = part[0];
-#pragma unroll
-                    for (int w = 1; w < kMaxWaves; ++w)
-                        v[f] += __uint_as_float(__float_as_uint(part[w]) & (w < W ? ~0u : 0u));
+                    v[f] = sum_waves(red + (f * NR + r) * 64 + lane, NU * NR * 64, W);
                 }
             }
             store_units<GATED, RH, 16>(a, t0 + 16 * m + NR * q + r, unit0 * 16 + row, v);
@@ -693,22 +719,260 @@ template <int XT, int G, bool GATED>
 hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
     if (a.t <= 4) return launch_units_mt<XT, G, GATED, 1, 1>(a, s);
     if (a.t <= 8) return launch_units_mt<XT, G, GATED, 1, 2>(a, s);
-    if (a.t <= 16) return launch_units_mt<XT, G, GATED, 1, 4>(a, s);
-    if (a.t <= 32) return launch_units_mt<XT, G, GATED, 2, 4>(a, s);
-    return launch_units_mt<XT, G, GATED, 4, 4>(a, s);
+    return launch_units_mt<XT, G, GATED, 1, 4>(a, s);
+}
+
+// ---------------------------------------------------------------- long chunks
+
+// Bound by the matrix core and the vector instructions beside it.  A workgroup
+// of 4 waves owns 128 rows and 256 outputs (gated: 128 of each matrix); a wave
+// owns two 32-output tiles for all 128 rows, so a code is expanded by one wave
+// only and serves four MFMAs, and a fragment of rows read from LDS serves two.
+//
+// Rows go to LDS by DMA, one 64-column step ahead, two buffers; 16-byte pieces
+// are exchanged within a row (XOR with the row number) so that a fragment's 32
+// rows fall into different banks.  Codes go to registers, one step ahead.
+//
+// Per group the 32 x 32 products of a tile take 4 MFMAs (130 cycles), adding
+// them up with their scale 16 multiply-adds (64 cycles).  The biases would
+// take as many again; instead they are a product of their own, group sums of
+// rows (three bf16 terms each, together exact to 24 bits) times biases (two
+// bf16 terms, exact), added by 5 MFMAs per tile and 16 groups.  Wave w sums
+// the rows of block w.
+//
+// Workgroups go to the 8 XCDs round-robin: XCD x takes the x-th eighth of the
+// (row block, output block) pairs, so its workgroups share rows and codes in
+// its L2.
+template <int G, bool GATED>
+__global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
+    constexpr int MT = 4, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
+    constexpr int XBUF = 128 * 128, SUMS = 3 * 128 * 32, BIAS = 2 * 32 * 32;  // BIAS: per wave
+    __shared__ __align__(128) uint8_t smem[2 * XBUF + 2 * SUMS + 4 * BIAS];
+    const uint32_t lds_base = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(smem));
+    const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nkb = a.k >> 6, obs = (a.n + 31) >> 5;
+    constexpr int TILES = GATED ? 4 : 8;  // 32-output tiles of a workgroup
+    const int nblk = (obs + TILES - 1) / TILES, total = nblk * ((a.t + 127) / 128);
+    const int share = (total + 7) >> 3, logical = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= share || logical >= total) return;
+    const int t0 = logical / nblk * 128, tile0 = logical % nblk * TILES + wave * (GATED ? 1 : 2);
+
+    // The wave's two tiles: code and scale sections of their tile row.  A tile
+    // past the matrix reads as zeros (an empty buffer) and stores nothing.
+    __amdgpu_buffer_rsrc_t wb[2], sb[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const uint8_t *rec = GATED && f ? a.record2 : a.record;
+        const int tile = GATED ? tile0 : tile0 + f;
+        const int steps = tile < obs ? nkb : 0;
+        wb[f] = buffer(rec + a.w + (size_t)min(tile, obs - 1) * nkb * 1024, steps * 1024);
+        sb[f] = buffer(rec + a.sb + (size_t)min(tile, obs - 1) * nkb * (128 * NG), steps * (128 * NG));
+    }
+    // DMA of rows: block j of 8 rows, lane s writes bytes 16 s of it, which
+    // hold piece (s % 8) ^ (row % 8) of row 8 j + s / 8.  Rows past the last
+    // repeat it.
+    const i32x4 rx = buffer_rsrc(a.x + (size_t)t0 * a.ldx_bytes);
+    uint32_t xvo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = (wave * 4 + j) * 8 + (lane >> 3);
+        xvo[j] = (uint32_t)min(r, a.t - 1 - t0) * (uint32_t)a.ldx_bytes + (uint32_t)(((lane & 7) ^ (r & 7)) * 16);
+    }
+    auto load_rows = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dma16(lds_base + (kb & 1) * XBUF + (wave * 4 + j) * 1024, xvo[j], rx, (uint32_t)kb * 128u);
+    };
+    u32x4 w[2];
+    uint32_t sv[2][NG];
+    auto load_codes = [&](int kb) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            w[f] = buffer_load16(wb[f], lane * 16, kb * 1024);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sv[f][g] = buffer_load4(sb[f], row * 4 + g * 128, kb * (128 * NG));
+        }
+    };
+    f32x16 acc[2][MT];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[f][m] = (f32x16){};
+    uint8_t *const sums = smem + 2 * XBUF, *const biases = sums + 2 * SUMS + wave * BIAS;
+    // Group sum v of row `row` of block `wave`: its three terms into slot `slot` of the chunk's buffer.
+    // (both lane halves write the same).
+    auto store_sum = [&](int chunk, int slot, float v) {
+        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * wave + row) * 32 + slot * 2;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+            const uint32_t h = __float_as_uint(v) & 0xffff0000u;
+            *reinterpret_cast<uint16_t *>(p + term * (128 * 32)) = (uint16_t)(h >> 16);
+            v -= __uint_as_float(h);
+        }
+    };
+    auto store_bias = [&](int f, int slot, uint16_t b) {
+        *reinterpret_cast<uint16_t *>(biases + (f * 32 + row) * 32 + slot * 2) = b;
+    };
+    // The biases' part of a chunk of 16 groups.
+    auto fold = [&](int chunk) {
+        bf16x8 bh[2], bl[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const u32x4 e = *reinterpret_cast<const u32x4 *>(biases + (f * 32 + row) * 32 + half * 16);
+            u32x4 h, l;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t pair = e[j];
+                const half2_t e2 = __builtin_bit_cast(half2_t, pair);
+                const float b0 = (float)e2.x, b1 = (float)e2.y;
+                const float h0 = __uint_as_float(__float_as_uint(b0) & 0xffff0000u), h1 = __uint_as_float(__float_as_uint(b1) & 0xffff0000u);
+                h[j] = __builtin_amdgcn_perm(__float_as_uint(h1), __float_as_uint(h0), 0x07060302u);
+                l[j] = __builtin_amdgcn_perm(__float_as_uint(b1 - h1), __float_as_uint(b0 - h0), 0x07060302u);
+            }
+            bh[f] = __builtin_bit_cast(bf16x8, h);
+            bl[f] = __builtin_bit_cast(bf16x8, l);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const uint8_t *p = sums + (chunk & 1) * SUMS + (32 * m + row) * 32 + half * 16;
+            const bf16x8 x0 = *reinterpret_cast<const bf16x8 *>(p);
+            const bf16x8 x1 = *reinterpret_cast<const bf16x8 *>(p + 128 * 32);
+            const bf16x8 x2 = *reinterpret_cast<const bf16x8 *>(p + 2 * 128 * 32);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                acc[f][m] = mfma_bf16(x2, bh[f], acc[f][m]);
+                acc[f][m] = mfma_bf16(x1, bl[f], acc[f][m]);
+                acc[f][m] = mfma_bf16(x1, bh[f], acc[f][m]);
+                acc[f][m] = mfma_bf16(x0, bl[f], acc[f][m]);
+                acc[f][m] = mfma_bf16(x0, bh[f], acc[f][m]);
+            }
+        }
+    };
+
+    load_rows(0);
+    load_codes(0);
+    for (int kb = 0; kb < nkb; ++kb) {
+        // this step's rows and codes are in; every wave is done with the buffer that the next step's rows go to
+        wait_vm<0>();
+        barrier_no_fence();
+        if (kb + 1 < nkb) load_rows(kb + 1);
+        if (kb > 0 && kb % CHUNK == 0) fold(kb / CHUNK - 1);
+        Frag wf[2];
+        float s[2][NG];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            wf[f] = w_frag<G>(w[f]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                s[f][g] = in_f32(__builtin_bit_cast(half2_t, sv[f][g]).x);
+                store_bias(f, kb % CHUNK * NG + g, (uint16_t)(sv[f][g] >> 16));
+            }
+        }
+        load_codes(min(kb + 1, nkb - 1));
+        const uint8_t *xb = smem + (kb & 1) * XBUF + row * 128;
+        // Products in order (block, group, tile); each one's multiply-adds run beside the next one's MFMAs.
+        // No branch in here: it would part the schedule, and every product of the step would wait at its end.
+        auto rows_of = [&](int m) {
+            Frag x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x.v[i] = *reinterpret_cast<const bf16x8 *>(xb + m * 4096 + ((piece_column<G>(i, half) / 8) ^ (row & 7)) * 16);
+            return x;
+        };
+        {
+            const Frag own = rows_of(wave);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float v = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (G == 64 || (i & 1) == g) {
+                        const u32x4 u = __builtin_bit_cast(u32x4, own.v[i]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v = add_pair(u[j], v);
+                    }
+                const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, __uint_as_float(both.x) + __uint_as_float(both.y));
+            }
+        }
+        Frag xf = rows_of(0);
+        f32x16 dp;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            Frag xn;
+#pragma unroll
+            for (int p = 0; p < 2 * NG; ++p) {
+                const int g = p / 2, f = p % 2;
+                const f32x16 d = group_product<G>(xf, wf[f], g);
+                if (p == 0 && m + 1 < MT) xn = rows_of(m + 1);
+                if (m || p) {
+                    const int pm = p ? m : m - 1, pg = p ? (p - 1) / 2 : NG - 1, pf = (p + 1) % 2;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[pf][pm][r] = __builtin_fmaf(s[pf][pg], dp[r], acc[pf][pm][r]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                dp = d;
+            }
+            xf = xn;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[1][MT - 1][r] = __builtin_fmaf(s[1][NG - 1], dp[r], acc[1][MT - 1][r]);
+    }
+    // the last chunk's missing groups
+    for (int slot = (nkb - 1) % CHUNK * NG + NG; slot < 16; ++slot) {
+        store_sum((nkb - 1) / CHUNK, slot, 0.0f);
+        store_bias(0, slot, 0);
+        store_bias(1, slot, 0);
+    }
+    barrier_no_fence();
+    fold((nkb - 1) / CHUNK);
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float v[2] = {acc[0][m][r], acc[1][m][r]};
+            store_units<GATED, GATED ? 1 : 2, 32>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), tile0 * 32 + row, v);
+        }
 }
 
 template <int XT, int G, bool GATED>
-hipError_t launch_few(const LinearArgs &a, hipStream_t s) {
-    if (a.t <= 64) return launch_units<XT, G, GATED>(a, s);
-    const unsigned obs = (unsigned)((a.n + 31) / 32);
-    hipLaunchKernelGGL((k_linear_few<XT, G, GATED, 4, 16, 4, 1>), dim3(obs, (a.t + 127) / 128), dim3(256), 0, s, a);
+hipError_t launch_many(const LinearArgs &a, hipStream_t s) {
+    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8;
+    const int total = (obs + tiles - 1) / tiles * ((a.t + 127) / 128);
+    hipLaunchKernelGGL((k_linear_many<G, GATED>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+#ifndef SPLIT_MT
+#define SPLIT_MT 1
+#define SPLIT_NT 2
+#endif
+template <int XT, int G, bool GATED, int MT, int NT>
+hipError_t launch_split_block(const LinearArgs &a, hipStream_t s) {
+    const int nkb = a.k >> 6;
+    int W = kMaxWaves;
+    while (W > 1 && W > nkb) W /= 2;
+    const dim3 grid((unsigned)(((a.n + 31) / 32 + NT - 1) / NT), (a.t + 32 * MT - 1) / (32 * MT));
+    const size_t lds = (size_t)W * (GATED ? 2 : NT) * 16 * 64 * 4;
+    hipLaunchKernelGGL((k_linear_split<XT, G, GATED, MT, NT>), grid, dim3(64 * W), lds, s, a);
+    return hipGetLastError();
+}
+template <int XT, int G, bool GATED>
+hipError_t launch_split(const LinearArgs &a, hipStream_t s) {
+    return launch_split_block<XT, G, GATED, SPLIT_MT, GATED ? 1 : SPLIT_NT>(a, s);
 }
 
 template <int XT, int G>
 hipError_t launch_gated(const LinearArgs &a, hipStream_t s) {
-    return a.record2 ? launch_few<XT, G, true>(a, s) : launch_few<XT, G, false>(a, s);
+#ifndef UMAX
+#define UMAX 16
+#define MANY_T 1024
+#endif
+    if (a.t <= UMAX) return a.record2 ? launch_units<XT, G, true>(a, s) : launch_units<XT, G, false>(a, s);
+    if constexpr (XT == MOE_BF16)
+        if (a.t >= MANY_T && a.ldx_bytes <= 1 << 24) return a.record2 ? launch_many<XT, G, true>(a, s) : launch_many<XT, G, false>(a, s);
+    return a.record2 ? launch_split<XT, G, true>(a, s) : launch_split<XT, G, false>(a, s);
 }
 
 template <int XT>
