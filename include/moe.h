@@ -507,7 +507,8 @@ moe_status moe_block_noalloc(const uint16_t *x, const float *w_router, int32_t t
  * the starts of consecutive rows, at least the row's width), so a slice of a
  * wider buffer's columns is passed as it is.  Rows that are read, and rows
  * of moe_residual_norm that are written, start 16-byte aligned (pointer and
- * stride); outputs of the projections are aligned to their element.  All
+ * stride) and are at most 2^22 elements apart; outputs of the projections
+ * are aligned to their element and at most 2^32 apart.  All
  * three calls are one kernel launch, need no workspace, keep no state and
  * give bitwise the same results for the same arguments.
  */

@@ -10,6 +10,10 @@
 namespace moe {
 namespace {
 
+// Largest row strides.  Rows that are read: 128 of them stay within 32-bit
+// byte offsets, which the kernels use inside a workgroup.
+constexpr int64_t kMaxStride = 1 << 22, kMaxOutStride = (int64_t)1 << 32;
+
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 size_t type_size(int type) { return type == MOE_F32 ? 4 : type == MOE_BF16 ? 2 : 1; }
@@ -41,9 +45,9 @@ moe_status check_t(int t, const char *who) {
 
 // A row matrix that is read or written 16 bytes at a time.
 moe_status check_rows16(const void *p, int64_t ld, int64_t width, int type, const char *who, const char *what) {
-    if (ld < width || ld > ((int64_t)1 << 40))
-        return fail(MOE_ERR_INVALID, "%s: row stride %lld of %s is below its width %lld (or above 2^40)", who,
-                    (long long)ld, what, (long long)width);
+    if (ld < width || ld > kMaxStride)
+        return fail(MOE_ERR_INVALID, "%s: row stride %lld of %s outside %lld..2^22", who, (long long)ld, what,
+                    (long long)width);
     if (!aligned(p, 16) || ld * type_size(type) % 16)
         return fail(MOE_ERR_INVALID, "%s: rows of %s must be 16-byte aligned (pointer and row stride)", who, what);
     return MOE_OK;
@@ -73,8 +77,8 @@ moe_status linear_args(LinearArgs &a, const void *x, int x_type, int64_t ldx, co
         return fail(MOE_ERR_INVALID, "%s: x_scale is null or misaligned", who);
     if (!aligned(record, 16) || !aligned(record2, 16))
         return fail(MOE_ERR_INVALID, "%s: records must be 16-byte aligned", who);
-    if (ldo < M->n || ldo > ((int64_t)1 << 40) || !aligned(out, type_size(out_type)))
-        return fail(MOE_ERR_INVALID, "%s: out is misaligned, or its row stride %lld is below n = %d (or above 2^40)", who,
+    if (ldo < M->n || ldo > kMaxOutStride || !aligned(out, type_size(out_type)))
+        return fail(MOE_ERR_INVALID, "%s: out is misaligned, or its row stride %lld is outside n = %d..2^32", who,
                     (long long)ldo, M->n);
     const Rows ro = rows(out, (size_t)M->n * type_size(out_type), (size_t)ldo * type_size(out_type));
     const Rows rx = rows(x, (size_t)M->k * type_size(x_type), (size_t)ldx * type_size(x_type));

@@ -25,6 +25,7 @@
 // of ones, in the accumulator's layout.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "lds_dma.h"
@@ -54,9 +55,15 @@ __device__ __forceinline__ u32x4 load16_once(const uint8_t *p) {
 __device__ __forceinline__ u32x2 load8(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL u32x2 *>(reinterpret_cast<uintptr_t>(p));
 }
-// A buffer of `bytes` bytes from p on (the same for every lane), and non-temporal loads from it.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
+// A buffer of `bytes` bytes from p on (the same for every lane), and loads from
+// it.  Every offset used here is inside the buffer: the hardware's range check
+// does not cover the scalar offset and is not relied on.
+// (The compiler loses track of that in 64-bit products, and would then loop over the lanes' buffers.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uintptr_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 constexpr int kNonTemporal = 2;
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
@@ -65,8 +72,15 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, uint32_
 __device__ __forceinline__ u32x2 buffer_load8(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, offset, kNonTemporal));
 }
+template <int HINT = 0>
 __device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
-    return __builtin_amdgcn_raw_buffer_load_b32(b, lane_offset, offset, kNonTemporal);
+    return __builtin_amdgcn_raw_buffer_load_b32(b, lane_offset, offset, HINT);
+}
+__device__ __forceinline__ u32x2 buffer_load8_plain(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, offset, 0));
+}
+__device__ __forceinline__ uint32_t buffer_load1(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
+    return __builtin_amdgcn_raw_buffer_load_b8(b, lane_offset, offset, 0);
 }
 __device__ __forceinline__ uint32_t load4_once(const uint8_t *p) {
     return __builtin_nontemporal_load(reinterpret_cast<const GLOBAL uint32_t *>(reinterpret_cast<uintptr_t>(p)));
@@ -123,50 +137,14 @@ __device__ __forceinline__ f32x16 mfma_bf16(bf16x8 a, bf16x8 b, f32x16 c) {
 // SiLU(g) * u; exp overflows to infinity for g below about -88, where the quotient is -0.
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
-// The rows of one 64-column step for one block of 32 tokens, as loaded.  Piece
-// i is 8 columns, the lane's part of the step's MFMA i: with groups of 64 the
-// pieces are a lane half's own 32 columns in order; with groups of 32, where
-// the MFMA's two lane halves have to belong to one group, pieces 0 2 are in
-// the first 32 columns and 1 3 in the second, alternating between the halves.
+// Column of piece i of a lane's rows in a 64-column step, 8 columns each, the
+// lane's part of the step's MFMA i: with groups of 64 the pieces are a lane
+// half's own 32 columns in order; with groups of 32, where the MFMA's two lane
+// halves have to belong to one group, pieces 0 2 are in the first 32 columns
+// and 1 3 in the second, alternating between the halves.
 template <int G>
 __device__ __forceinline__ int piece_column(int i, int half) {
     return G == 64 ? 32 * half + 8 * i : 32 * (i & 1) + 16 * (i >> 1) + 8 * half;
-}
-template <int XT>
-struct XRaw;
-template <>
-struct XRaw<MOE_BF16> {
-    u32x4 v[4];
-};
-template <>
-struct XRaw<MOE_E4M3> {
-    u32x2 v[4];
-    uint32_t scale[2];  // of the step's two 32-column blocks
-};
-
-// p: the token's row; scale: its block scales (or any bytes that may be read).
-template <int XT, int G>
-__device__ __forceinline__ XRaw<XT> load_x(const uint8_t *p, int kb, int half, const uint8_t *scale) {
-    XRaw<XT> f;
-    if constexpr (XT == MOE_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.v[i] = load16(p + kb * 128 + 2 * piece_column<G>(i, half));
-    } else {
-        p += kb * 64;
-        if constexpr (G == 64) {
-            const u32x4 a = load16(p + 32 * half), b = load16(p + 32 * half + 16);
-            f.v[0] = (u32x2){a.x, a.y};
-            f.v[1] = (u32x2){a.z, a.w};
-            f.v[2] = (u32x2){b.x, b.y};
-            f.v[3] = (u32x2){b.z, b.w};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f.v[i] = load8(p + piece_column<G>(i, half));
-        }
-        f.scale[0] = load1(scale + kb * 2 + (G == 64 ? half : 0));
-        f.scale[1] = G == 64 ? 0 : load1(scale + kb * 2 + 1);
-    }
-    return f;
 }
 
 // 8 e4m3 values times a power of two, as bf16.
@@ -182,13 +160,27 @@ __device__ __forceinline__ bf16x8 e4m3_bf16(u32x2 v, float scale) {
 struct Frag {
     bf16x8 v[4];
 };
+
+// Rows of a step in LDS, written by DMA: 64 columns of each row, its 16-byte
+// parts exchanged so that one part of 8 neighbouring rows falls into different
+// banks.  part_at: where part p of row r is, relative to the row.
+template <int XT>
+__device__ __forceinline__ int part_at(int p, int r) {
+    return (XT == MOE_BF16 ? p ^ (r & 7) : p ^ ((r >> 1) & 3)) * 16;
+}
+template <int XT>
+constexpr int kRowBytes = XT == MOE_BF16 ? 128 : 64;
+
+// The lane's operands from `p`, row r's 64 columns; scale: of the first and
+// second 32 columns (e4m3; with groups of 64 the lane half's own, twice).
 template <int XT, int G>
-__device__ __forceinline__ Frag x_frag(const XRaw<XT> &x, bool block_scales) {
+__device__ __forceinline__ Frag x_frag(const uint8_t *p, int r, int half, const float scale[2]) {
     Frag f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (XT == MOE_BF16) f.v[i] = __builtin_bit_cast(bf16x8, x.v[i]);
-        else f.v[i] = e4m3_bf16(x.v[i], __uint_as_float((block_scales ? x.scale[G == 64 ? 0 : i & 1] : 127u) << 23));
+        const int c = piece_column<G>(i, half);
+        if constexpr (XT == MOE_BF16) f.v[i] = *reinterpret_cast<const bf16x8 *>(p + part_at<XT>(c / 8, r));
+        else f.v[i] = e4m3_bf16(*reinterpret_cast<const u32x2 *>(p + part_at<XT>(c / 16, r) + c % 16), scale[G == 64 ? 0 : i & 1]);
     }
     return f;
 }
@@ -306,34 +298,46 @@ __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int co
 // ---------------------------------------------------------------- some hundred rows
 
 // Too few output tiles to fill the chip with long-running workgroups, so the
-// waves of a workgroup split the 64-column steps (wave w takes steps w, w + W,
-// ...) of one output block, 32 MT rows by NT tiles of 32 outputs (gated: one
-// tile of each matrix), and their sums meet in LDS, added in wave order.  A
-// wave reads its rows and codes straight from the cache into registers, the
-// next step's while this one computes.  Rows past the last load the last
-// row's values and store nothing; steps past the last repeat it with scale and
-// bias 0.
+// waves of a workgroup split the 64-column steps of one output block, 32 MT
+// rows by NT tiles of 32 outputs (gated: one tile of each matrix): wave w
+// takes the w-th run of steps, and the waves' sums meet in LDS, added in wave
+// order.  Waves do not wait for each other before that.
+//
+// A wave's rows come by DMA into LDS of its own, 128 (e4m3: 64) adjacent bytes
+// of a row at a time; loaded straight into the operand's lanes, 16 bytes here
+// and there, they took four times as long in the address unit and bound the
+// kernel.  Codes go to registers.  Both are loaded one step ahead.  Rows past
+// the last repeat it and store nothing.
 template <int XT, int G, bool GATED, int MT, int NT>
 __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
     static_assert(!GATED || NT == 1, "a gated workgroup has one tile of each matrix");
     constexpr int NM = GATED ? 2 : 1, NW = NM * NT, NG = 64 / G;
-    extern __shared__ float red[];  // [waves][NW][16][64]
+    constexpr int ROW = kRowBytes<XT>, XBUF = 32 * MT * ROW, LOADS = XBUF / 1024, PER = 1024 / ROW;
+    extern __shared__ __align__(128) uint8_t split_lds[];  // [waves][2][XBUF] rows; then [waves][NW][16][64] sums
+    const uint32_t lds_base = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(split_lds));
     const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
     const int ob = blockIdx.x * NT, t0 = blockIdx.y * 32 * MT;
-    const int nkb = a.k >> 6;
+    const int nkb = a.k >> 6, run = (nkb + W - 1) / W, k0 = wave * run, k1 = min(k0 + run, nkb);
 
     const bool block_scales = a.x_scale_kind == MOE_SCALE_BLOCK;
-    const uint8_t *xp[MT], *xs[MT];
+    const int rows = min(a.t - t0, 32 * MT);
+    const i32x4 rx = buffer_rsrc(a.x + (size_t)t0 * a.ldx_bytes);
+    // load j: PER rows; lane s writes bytes 16 s of them, a part of row PER j + s / (64 / PER)
+    uint32_t xvo[LOADS];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = min(t0 + 32 * m + row, a.t - 1);
-        xp[m] = a.x + (size_t)r * a.ldx_bytes;
-        // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
-        xs[m] = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : xp[m];
+    for (int j = 0; j < LOADS; ++j) {
+        const int r = PER * j + lane / (64 / PER);
+        xvo[j] = (uint32_t)min(r, rows - 1) * (uint32_t)a.ldx_bytes + part_at<XT>(lane % (64 / PER), r);
     }
-    // a second tile past the matrix is outside the buffer: its codes and scales read as 0
-    const int tiles = min(NT, ((a.n + 31) >> 5) - ob) * nkb;
+    const uint32_t srow = a.k >> 5;
+    const __amdgpu_buffer_rsrc_t xsb = buffer(block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)t0 * srow : a.x,
+                                              rows * srow);
+    uint32_t sat[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sat[m] = min(32 * m + row, rows - 1) * srow;
+    // a second tile past the matrix is the first one again (its outputs are not stored)
+    const int tiles = min(NT, ((a.n + 31) >> 5) - ob) * nkb, next = tiles - nkb;
     __amdgpu_buffer_rsrc_t wb[NM], sb[NM];
 #pragma unroll
     for (int f = 0; f < NM; ++f) {
@@ -344,19 +348,28 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
     struct Batch {
         u32x4 w[NW];
         uint32_t sb[NW][NG];
-        XRaw<XT> x[MT];
+        uint32_t scale[MT][2];
     };
-    auto load = [&](Batch &b, int k0) {
-        const int kb = min(k0, nkb - 1);
+    auto load = [&](Batch &b, int kb) {
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds_base + (wave * 2 + (kb & 1)) * XBUF);
+        const uint32_t from = __builtin_amdgcn_readfirstlane((uint32_t)kb * ROW);
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) dma16(to + j * 1024, xvo[j], rx, from);
 #pragma unroll
         for (int f = 0; f < NW; ++f) {
-            const int at = kb + (f % NT) * nkb;
+            const int at = kb + (f % NT ? next : 0);
             b.w[f] = buffer_load16(wb[f / NT], lane * 16, at * 1024);
 #pragma unroll
             for (int g = 0; g < NG; ++g) b.sb[f][g] = buffer_load4(sb[f / NT], row * 4 + g * 128, at * (128 * NG));
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) b.x[m] = load_x<XT, G>(xp[m], kb, half, xs[m]);
+        for (int m = 0; m < MT; ++m) {
+            b.scale[m][0] = b.scale[m][1] = 127;
+            if (XT == MOE_E4M3 && block_scales) {
+                b.scale[m][0] = buffer_load1(xsb, sat[m] + (G == 64 ? half : 0), kb * 2);
+                if (G == 32) b.scale[m][1] = buffer_load1(xsb, sat[m] + 1, kb * 2);
+            }
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
     f32x16 acc[NW][MT];
@@ -364,13 +377,15 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
     for (int f = 0; f < NW; ++f)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[f][m] = (f32x16){};
-    auto compute = [&](const Batch &b) {
+    auto compute = [&](const Batch &b, int kb) {
         Frag wf[NW];
 #pragma unroll
         for (int f = 0; f < NW; ++f) wf[f] = w_frag<G>(b.w[f]);
+        const uint8_t *xl = split_lds + (wave * 2 + (kb & 1)) * XBUF + row * ROW;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const Frag xf = x_frag<XT, G>(b.x[m], block_scales);
+            const float scale[2] = {__uint_as_float(b.scale[m][0] << 23), __uint_as_float(b.scale[m][1] << 23)};
+            const Frag xf = x_frag<XT, G>(xl + m * 32 * ROW, row, half, scale);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const f32x16 xsum = group_sum<G>(xf, g);
@@ -386,25 +401,26 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
             }
         }
     };
-    if (wave < nkb) {
+    if (k0 < k1) {
         Batch b0, b1;
-        int kb = wave;
+        int kb = k0;
         load(b0, kb);
         while (true) {
-            if (kb + W >= nkb) { compute(b0); break; }
-            load(b1, kb + W);
-            compute(b0);
-            kb += W;
-            if (kb + W >= nkb) { compute(b1); break; }
-            load(b0, kb + W);
-            compute(b1);
-            kb += W;
+            wait_vm<0>();
+            if (kb + 1 < k1) load(b1, kb + 1);
+            compute(b0, kb);
+            if (++kb >= k1) break;
+            wait_vm<0>();
+            if (kb + 1 < k1) load(b0, kb + 1);
+            compute(b1, kb);
+            if (++kb >= k1) break;
         }
     }
 
+    float *red = reinterpret_cast<float *>(split_lds);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        if (m) __syncthreads();
+        __syncthreads();  // rows (or the block before) are read
 #pragma unroll
         for (int f = 0; f < NW; ++f)
 #pragma unroll
@@ -544,9 +560,9 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
 #pragma unroll
             for (int f = 0; f < NU; ++f) {
                 if constexpr (G == 64) b.w[u][f] = buffer_load8(wb[f / RH], wo[f % RH], kb * 1024);
-                else b.w[u][f] = (u32x2){buffer_load4(wb[f / RH], wo[f % RH], kb * 1024), buffer_load4(wb[f / RH], wo[f % RH] + 512, kb * 1024)};
+                else b.w[u][f] = (u32x2){buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH], kb * 1024), buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH] + 512, kb * 1024)};
 #pragma unroll
-                for (int g = 0; g < NG; ++g) b.sb[u][f][g] = buffer_load4(sb[f / RH], so[f % RH] + g * 128, kb * (128 * NG));
+                for (int g = 0; g < NG; ++g) b.sb[u][f][g] = buffer_load4<kNonTemporal>(sb[f / RH], so[f % RH] + g * 128, kb * (128 * NG));
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -759,15 +775,14 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     const int t0 = logical / nblk * 128, tile0 = logical % nblk * TILES + wave * (GATED ? 1 : 2);
 
     // The wave's two tiles: code and scale sections of their tile row.  A tile
-    // past the matrix reads as zeros (an empty buffer) and stores nothing.
+    // past the matrix is the last one again and stores nothing.
     __amdgpu_buffer_rsrc_t wb[2], sb[2];
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
         const uint8_t *rec = GATED && f ? a.record2 : a.record;
         const int tile = GATED ? tile0 : tile0 + f;
-        const int steps = tile < obs ? nkb : 0;
-        wb[f] = buffer(rec + a.w + (size_t)min(tile, obs - 1) * nkb * 1024, steps * 1024);
-        sb[f] = buffer(rec + a.sb + (size_t)min(tile, obs - 1) * nkb * (128 * NG), steps * (128 * NG));
+        wb[f] = buffer(rec + a.w + (size_t)min(tile, obs - 1) * nkb * 1024, nkb * 1024);
+        sb[f] = buffer(rec + a.sb + (size_t)min(tile, obs - 1) * nkb * (128 * NG), nkb * (128 * NG));
     }
     // DMA of rows: block j of 8 rows, lane s writes bytes 16 s of it, which
     // hold piece (s % 8) ^ (row % 8) of row 8 j + s / 8.  Rows past the last
@@ -951,10 +966,13 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t s) {
 template <int XT, int G, bool GATED, int MT, int NT>
 hipError_t launch_split_block(const LinearArgs &a, hipStream_t s) {
     const int nkb = a.k >> 6;
-    int W = kMaxWaves;
+#ifndef SPW
+#define SPW kMaxWaves
+#endif
+    int W = SPW;
     while (W > 1 && W > nkb) W /= 2;
     const dim3 grid((unsigned)(((a.n + 31) / 32 + NT - 1) / NT), (a.t + 32 * MT - 1) / (32 * MT));
-    const size_t lds = (size_t)W * (GATED ? 2 : NT) * 16 * 64 * 4;
+    const size_t lds = (size_t)W * std::max((GATED ? 2 : NT) * 16 * 64 * 4, 2 * 32 * MT * kRowBytes<XT>);
     hipLaunchKernelGGL((k_linear_split<XT, G, GATED, MT, NT>), grid, dim3(64 * W), lds, s, a);
     return hipGetLastError();
 }

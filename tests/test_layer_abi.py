@@ -96,7 +96,7 @@ LINEAR_BAD = [
     (dict(x_type=mep.F32), INVALID), (dict(x_type=7), INVALID), (dict(out_type=mep.E4M3), INVALID),
     (dict(out_type=-1), INVALID), (dict(ldx=255), INVALID), (dict(ldx=260), INVALID), (dict(ldx=-256), INVALID),
     (dict(x=X + 8), INVALID), (dict(rec=REC + 4), INVALID), (dict(ldo=95), INVALID), (dict(out=OUT + 2), INVALID),
-    (dict(ldo=1 << 41), INVALID), (dict(xsk=1, xs=XS), INVALID),                     # bf16 rows have no scales
+    (dict(ldo=1 << 41), INVALID), (dict(ldx=(1 << 22) + 8), INVALID), (dict(xsk=1, xs=XS), INVALID),                     # bf16 rows have no scales
     (dict(x_type=mep.E4M3, xsk=3, xs=XS), INVALID), (dict(x_type=mep.E4M3, xsk=1), INVALID),
     (dict(x_type=mep.E4M3, xsk=1, xs=XS + 2), INVALID), (dict(x_type=mep.E4M3, ldx=264), INVALID),
     (dict(out=X), INVALID), (dict(out=X + 3 * 512 + 508), INVALID), (dict(out=X - 4 * 96 * 4 + 4), INVALID),
