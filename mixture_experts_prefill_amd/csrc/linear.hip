@@ -44,6 +44,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 #define GLOBAL __attribute__((address_space(1)))
 
 __device__ __forceinline__ u32x4 load16(const uint8_t *p) {
@@ -134,6 +135,12 @@ __device__ __forceinline__ float add_pair(uint32_t u, float v) {
 __device__ __forceinline__ f32x16 mfma_bf16(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+// e4m3 operands, each lane's first and second 16 values scaled by 2^(scale - 127).
+__device__ __forceinline__ f32x16 mfma_e4m3(i32x8 a, i32x8 b, f32x16 c, int a_scale, int b_scale) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, a_scale, 0, b_scale);
+}
+constexpr int kScaleOne = 127, kScaleCode = 127 + 9;
+
 // SiLU(g) * u; exp overflows to infinity for g below about -88, where the quotient is -0.
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
@@ -171,17 +178,32 @@ __device__ __forceinline__ int part_at(int p, int r) {
 template <int XT>
 constexpr int kRowBytes = XT == MOE_BF16 ? 128 : 64;
 
-// The lane's operands from `p`, row r's 64 columns; scale: of the first and
-// second 32 columns (e4m3; with groups of 64 the lane half's own, twice).
+// A lane's pieces in LDS.  piece_at: where its piece 0 is, relative to its row;
+// the part of piece i differs from that of piece 0 by an XOR that is the same
+// for every lane, so one address a lane finds all of them.
 template <int XT, int G>
-__device__ __forceinline__ Frag x_frag(const uint8_t *p, int r, int half, const float scale[2]) {
+__device__ __forceinline__ int piece_at(int r, int half) {
+    const int c = piece_column<G>(0, half);
+    return XT == MOE_BF16 ? part_at<XT>(c / 8, r) : part_at<XT>(c / 16, r) + c % 16;
+}
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *(const LOCAL T *)at;
+}
+// The operand of piece i from the LDS address of piece 0; scale: of the first
+// and second 32 columns (e4m3; with groups of 64 the lane half's own).
+template <int XT, int G>
+__device__ __forceinline__ bf16x8 x_piece(uint32_t at, int i, const float scale[2]) {
+    const int c = piece_column<G>(i, 0), part = XT == MOE_BF16 ? c / 8 : c / 16;  // of half 0, whose piece 0 is at column 0
+    at ^= part * 16;
+    if constexpr (XT == MOE_BF16) return lds_read<bf16x8>(at);
+    else return e4m3_bf16(lds_read<u32x2>(at + (G == 64 ? c % 16 : 0)), scale[G == 64 ? 0 : i & 1]);
+}
+template <int XT, int G>
+__device__ __forceinline__ Frag x_frag(uint32_t at, const float scale[2]) {
     Frag f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = piece_column<G>(i, half);
-        if constexpr (XT == MOE_BF16) f.v[i] = *reinterpret_cast<const bf16x8 *>(p + part_at<XT>(c / 8, r));
-        else f.v[i] = e4m3_bf16(*reinterpret_cast<const u32x2 *>(p + part_at<XT>(c / 16, r) + c % 16), scale[G == 64 ? 0 : i & 1]);
-    }
+    for (int i = 0; i < 4; ++i) f.v[i] = x_piece<XT, G>(at, i, scale);
     return f;
 }
 
@@ -221,6 +243,29 @@ __device__ __forceinline__ f32x16 group_sum(const Frag &x, int gi) {
     for (int i = 0; i < 4; ++i)
         if (G == 64 || (i & 1) == gi) d = mfma_bf16(x.v[i], one, d);
     return d;
+}
+
+// The operands of the e4m3 MFMA (32x32x64).  The lane halves take alternate 16
+// bytes of a step's 64 columns: a lane's first 16 bytes belong to the first 32
+// columns, the others to the second, and the scale operand of lane half h is
+// that of the h-th 32 columns.  Codes: a byte 0..15 is q * 2^-9, the scale
+// brings 2^9; words are exchanged between the lane halves first.
+__device__ __forceinline__ i32x8 w_frag8(u32x4 w) {
+    const u32x2 p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+    const u32x2 q = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+    const u32x2 a = code_bytes(p.x), b = code_bytes(q.x), c = code_bytes(p.y), d = code_bytes(q.y);
+    return (i32x8){(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
+}
+// at: LDS address of the lane's first 16 bytes (part `half`).
+__device__ __forceinline__ i32x8 x_frag8(uint32_t at) {
+    const u32x4 a = lds_read<u32x4>(at), b = lds_read<u32x4>(at ^ 32);
+    return (i32x8){(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+// Group gi alone (groups of 32): the other one's 16 bytes 0.
+template <int G>
+__device__ __forceinline__ i32x8 group_of(i32x8 v, int gi) {
+    if (G == 64) return v;
+    return gi ? (i32x8){0, 0, 0, 0, v[4], v[5], v[6], v[7]} : (i32x8){v[0], v[1], v[2], v[3], 0, 0, 0, 0};
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -381,11 +426,11 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
         Frag wf[NW];
 #pragma unroll
         for (int f = 0; f < NW; ++f) wf[f] = w_frag<G>(b.w[f]);
-        const uint8_t *xl = split_lds + (wave * 2 + (kb & 1)) * XBUF + row * ROW;
+        const uint32_t xl = lds_base + (wave * 2 + (kb & 1)) * XBUF + row * ROW + piece_at<XT, G>(row, half);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const float scale[2] = {__uint_as_float(b.scale[m][0] << 23), __uint_as_float(b.scale[m][1] << 23)};
-            const Frag xf = x_frag<XT, G>(xl + m * 32 * ROW, row, half, scale);
+            const Frag xf = x_frag<XT, G>(xl + m * 32 * ROW, scale);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const f32x16 xsum = group_sum<G>(xf, g);
@@ -759,20 +804,24 @@ hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
 // Workgroups go to the 8 XCDs round-robin: XCD x takes the x-th eighth of the
 // (row block, output block) pairs, so its workgroups share rows and codes in
 // its L2.
-template <int G, bool GATED>
-__global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
-    constexpr int MT = 4, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
-    constexpr int XBUF = 128 * 128, SUMS = 3 * 128 * 32, BIAS = 2 * 32 * 32;  // BIAS: per wave
-    __shared__ __align__(128) uint8_t smem[2 * XBUF + 2 * SUMS + 4 * BIAS];
+template <int XT, int G, bool GATED, bool F8, int MT>
+__global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs a) {
+    static_assert(!F8 || XT == MOE_E4M3, "e4m3 products are of e4m3 rows");
+    static_assert(F8 || MT == 4, "the four waves sum a block of rows each, a piece beside each block's products");
+    constexpr int BM = 32 * MT, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
+    constexpr int ROW = kRowBytes<XT>, XBUF = BM * ROW, LOADS = XBUF / 4096, PER = 1024 / ROW;  // a wave's loads, rows of one
+    constexpr int SUMS = 3 * BM * 32, BIAS = 2 * 32 * 32;  // of a chunk; BIAS: per wave
+    constexpr int SCALES = XT == MOE_E4M3 ? BM * 8 : 0;     // block scales of a step: u32 [BM][2]
+    __shared__ __align__(128) uint8_t smem[2 * XBUF + 2 * SUMS + 8 * BIAS + 2 * SCALES + 256 * 16];
     const uint32_t lds_base = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(smem));
     const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nkb = a.k >> 6, obs = (a.n + 31) >> 5;
     constexpr int TILES = GATED ? 4 : 8;  // 32-output tiles of a workgroup
-    const int nblk = (obs + TILES - 1) / TILES, total = nblk * ((a.t + 127) / 128);
+    const int nblk = (obs + TILES - 1) / TILES, total = nblk * ((a.t + BM - 1) / BM);
     const int share = (total + 7) >> 3, logical = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= share || logical >= total) return;
-    const int t0 = logical / nblk * 128, tile0 = logical % nblk * TILES + wave * (GATED ? 1 : 2);
+    const int t0 = logical / nblk * BM, tile0 = logical % nblk * TILES + wave * (GATED ? 1 : 2);
 
     // The wave's two tiles: code and scale sections of their tile row.  A tile
     // past the matrix is the last one again and stores nothing.
@@ -784,20 +833,36 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         wb[f] = buffer(rec + a.w + (size_t)min(tile, obs - 1) * nkb * 1024, nkb * 1024);
         sb[f] = buffer(rec + a.sb + (size_t)min(tile, obs - 1) * nkb * (128 * NG), nkb * (128 * NG));
     }
-    // DMA of rows: block j of 8 rows, lane s writes bytes 16 s of it, which
-    // hold piece (s % 8) ^ (row % 8) of row 8 j + s / 8.  Rows past the last
-    // repeat it.
+    // DMA of rows: load j brings PER rows; lane s writes bytes 16 s of them, a
+    // part of row PER j + s / (64 / PER).  Rows past the last repeat it.  Block
+    // scales: one load a wave, lane s those of row s / 2, block s % 2, as words.
+    const int rows = min(a.t - t0, BM);
     const i32x4 rx = buffer_rsrc(a.x + (size_t)t0 * a.ldx_bytes);
-    uint32_t xvo[4];
+    // (Its lane offsets wait in LDS between the steps: there are no registers to spare.)
+    constexpr int OFFSETS_AT = 2 * XBUF + 2 * SUMS + 8 * BIAS + 2 * SCALES;
+    u32x4 *const offsets = reinterpret_cast<u32x4 *>(smem + OFFSETS_AT) + threadIdx.x;
+    {
+        u32x4 o = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = (wave * 4 + j) * 8 + (lane >> 3);
-        xvo[j] = (uint32_t)min(r, a.t - 1 - t0) * (uint32_t)a.ldx_bytes + (uint32_t)(((lane & 7) ^ (r & 7)) * 16);
+        for (int j = 0; j < LOADS; ++j) {
+            const int r = (wave * LOADS + j) * PER + lane / (64 / PER);
+            o[j] = (uint32_t)min(r, rows - 1) * (uint32_t)a.ldx_bytes + part_at<XT>(lane % (64 / PER), r);
+        }
+        *offsets = o;
     }
+    const bool block_scales = XT == MOE_E4M3 && a.x_scale_kind == MOE_SCALE_BLOCK;
+    const uint32_t srow = a.k >> 5, scales_at = 2 * XBUF + 2 * SUMS + 8 * BIAS;
+    const i32x4 rxs = buffer_rsrc(block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)t0 * srow : a.x);
+    const uint32_t svo = (uint32_t)min(32 * (wave % MT) + (lane >> 1), rows - 1) * srow + (lane & 1);
     auto load_rows = [&](int kb) {
+        const u32x4 o = *offsets;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dma16(lds_base + (kb & 1) * XBUF + (wave * 4 + j) * 1024, xvo[j], rx, (uint32_t)kb * 128u);
+        for (int j = 0; j < LOADS; ++j)
+            dma16(lds_base + (kb & 1) * XBUF + (wave * LOADS + j) * 1024, o[j], rx, (uint32_t)kb * ROW);
+        if (block_scales && (MT == 4 || wave < MT)) dma1(lds_base + scales_at + (kb & 1) * SCALES + wave * 256, svo, rxs, (uint32_t)kb * 2u);
     };
+    if (XT == MOE_E4M3 && !block_scales)
+        for (int i = threadIdx.x; i < 2 * SCALES / 4; i += 256) reinterpret_cast<uint32_t *>(smem + scales_at)[i] = kScaleOne;
     u32x4 w[2];
     uint32_t sv[2][NG];
     auto load_codes = [&](int kb) {
@@ -808,32 +873,33 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
             for (int g = 0; g < NG; ++g) sv[f][g] = buffer_load4(sb[f], row * 4 + g * 128, kb * (128 * NG));
         }
     };
+    const uint32_t x_at = lds_base + row * ROW + (F8 ? part_at<XT>(half, row) : piece_at<XT, G>(row, half));
     f32x16 acc[2][MT];
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[f][m] = (f32x16){};
-    uint8_t *const sums = smem + 2 * XBUF, *const biases = sums + 2 * SUMS + wave * BIAS;
+    uint8_t *const sums = smem + 2 * XBUF, *const biases = sums + 2 * SUMS + wave * (2 * BIAS);
     // Group sum v of row `row` of block `wave`: its three terms into slot `slot` of the chunk's buffer.
     // (both lane halves write the same).
     auto store_sum = [&](int chunk, int slot, float v) {
-        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * wave + row) * 32 + slot * 2;
+        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * (wave % MT) + row) * 32 + slot * 2;
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
             const uint32_t h = __float_as_uint(v) & 0xffff0000u;
-            *reinterpret_cast<uint16_t *>(p + term * (128 * 32)) = (uint16_t)(h >> 16);
+            *reinterpret_cast<uint16_t *>(p + term * (BM * 32)) = (uint16_t)(h >> 16);
             v -= __uint_as_float(h);
         }
     };
-    auto store_bias = [&](int f, int slot, uint16_t b) {
-        *reinterpret_cast<uint16_t *>(biases + (f * 32 + row) * 32 + slot * 2) = b;
+    auto store_bias = [&](int chunk, int f, int slot, uint16_t b) {
+        *reinterpret_cast<uint16_t *>(biases + (chunk & 1) * BIAS + (f * 32 + row) * 32 + slot * 2) = b;
     };
     // The biases' part of a chunk of 16 groups.
     auto fold = [&](int chunk) {
         bf16x8 bh[2], bl[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const u32x4 e = *reinterpret_cast<const u32x4 *>(biases + (f * 32 + row) * 32 + half * 16);
+            const u32x4 e = *reinterpret_cast<const u32x4 *>(biases + (chunk & 1) * BIAS + (f * 32 + row) * 32 + half * 16);
             u32x4 h, l;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -851,8 +917,8 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         for (int m = 0; m < MT; ++m) {
             const uint8_t *p = sums + (chunk & 1) * SUMS + (32 * m + row) * 32 + half * 16;
             const bf16x8 x0 = *reinterpret_cast<const bf16x8 *>(p);
-            const bf16x8 x1 = *reinterpret_cast<const bf16x8 *>(p + 128 * 32);
-            const bf16x8 x2 = *reinterpret_cast<const bf16x8 *>(p + 2 * 128 * 32);
+            const bf16x8 x1 = *reinterpret_cast<const bf16x8 *>(p + BM * 32);
+            const bf16x8 x2 = *reinterpret_cast<const bf16x8 *>(p + 2 * BM * 32);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 acc[f][m] = mfma_bf16(x2, bh[f], acc[f][m]);
@@ -864,67 +930,111 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
     };
 
-    load_rows(0);
-    load_codes(0);
-    for (int kb = 0; kb < nkb; ++kb) {
-        // this step's rows and codes are in; every wave is done with the buffer that the next step's rows go to
-        wait_vm<0>();
-        barrier_no_fence();
-        if (kb + 1 < nkb) load_rows(kb + 1);
-        if (kb > 0 && kb % CHUNK == 0) fold(kb / CHUNK - 1);
-        Frag wf[2];
-        float s[2][NG];
+    // Step kb's codes, loaded, as operands.
+    typename std::conditional<F8, i32x8, Frag>::type wf[2];
+    float s[2][NG];
+    auto expand = [&](int kb) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            wf[f] = w_frag<G>(w[f]);
+            if constexpr (F8) wf[f] = w_frag8(w[f]);
+            else wf[f] = w_frag<G>(w[f]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 s[f][g] = in_f32(__builtin_bit_cast(half2_t, sv[f][g]).x);
-                store_bias(f, kb % CHUNK * NG + g, (uint16_t)(sv[f][g] >> 16));
+                store_bias(kb / CHUNK, f, kb % CHUNK * NG + g, (uint16_t)(sv[f][g] >> 16));
             }
         }
-        load_codes(min(kb + 1, nkb - 1));
-        const uint8_t *xb = smem + (kb & 1) * XBUF + row * 128;
-        // Products in order (block, group, tile); each one's multiply-adds run beside the next one's MFMAs.
-        // No branch in here: it would part the schedule, and every product of the step would wait at its end.
+    };
+
+    // Rows are loaded at the start of the step before their own; codes at the
+    // end of the step but one before, expanded at the end of the step before.
+    constexpr int CODE_LOADS = 2 * (1 + NG);
+    load_rows(0);
+    load_codes(0);
+    expand(0);
+    load_codes(min(1, nkb - 1));
+    for (int kb = 0; kb < nkb; ++kb) {
+        // this step's rows are in (only the next codes, loaded after them, may be on their way); every wave is
+        // done with the buffer that the next step's rows go to
+        wait_vm<CODE_LOADS>();
+        barrier_no_fence();
+        if (kb + 1 < nkb) load_rows(kb + 1);
+        if (kb > 0 && kb % CHUNK == 0) fold(kb / CHUNK - 1);
+        // (an address only: kept from being split into loop constants, for which there are no registers)
+        uint32_t xb = x_at;
+        asm volatile("" : "+v"(xb));
+        xb += (kb & 1) * XBUF;
+        const uint32_t *xsb = reinterpret_cast<const uint32_t *>(smem + scales_at + (kb & 1) * SCALES) + row * 2;
+        // Rows of block m as operands.  No branch in here: it would part the
+        // schedule, and every product of the step would wait at its end.
+        struct Rows {
+            typename std::conditional<F8, i32x8, Frag>::type v;
+            int scale;
+        };
         auto rows_of = [&](int m) {
-            Frag x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x.v[i] = *reinterpret_cast<const bf16x8 *>(xb + m * 4096 + ((piece_column<G>(i, half) / 8) ^ (row & 7)) * 16);
+            Rows x;
+            x.scale = kScaleOne;
+            if constexpr (F8) {
+                x.v = x_frag8(xb + m * 32 * ROW);
+                x.scale = (int)xsb[m * 64 + half];
+            } else {
+                float scale[2] = {1.0f, 1.0f};
+                if constexpr (XT == MOE_E4M3) {
+                    scale[0] = __uint_as_float(xsb[m * 64 + (G == 64 ? half : 0)] << 23);
+                    scale[1] = G == 64 ? scale[0] : __uint_as_float(xsb[m * 64 + 1] << 23);
+                }
+                x.v = x_frag<XT, G>(xb + m * 32 * ROW, scale);
+            }
             return x;
         };
-        {
-            const Frag own = rows_of(wave);
+        // The wave's own block's group sums.  e4m3: one more product, with ones.  Otherwise piece by piece
+        // beside the products: piece m with block m's.
+        float sum[NG];
+        if constexpr (F8) {
+            if (MT == 4 || wave < MT) {
+                const Rows own = rows_of(wave);
+                constexpr int o = 0x38383838;  // 1.0
+                const i32x8 one = {o, o, o, o, o, o, o, o};
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float v = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (G == 64 || (i & 1) == g) {
-                        const u32x4 u = __builtin_bit_cast(u32x4, own.v[i]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v = add_pair(u[j], v);
-                    }
-                const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, __uint_as_float(both.x) + __uint_as_float(both.y));
+                for (int g = 0; g < NG; ++g)
+                    store_sum(kb / CHUNK, (kb % CHUNK) * NG + g,
+                              mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0]);
             }
+        } else {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
         }
-        Frag xf = rows_of(0);
+        float own_scale[2] = {1.0f, 1.0f};
+        if constexpr (!F8 && XT == MOE_E4M3) {
+            own_scale[0] = __uint_as_float(xsb[wave * 64 + (G == 64 ? half : 0)] << 23);
+            own_scale[1] = G == 64 ? own_scale[0] : __uint_as_float(xsb[wave * 64 + 1] << 23);
+        }
+        // Products in order (block, group, tile); each one's multiply-adds run beside the next one's MFMAs.
+        Rows xf = rows_of(0);
         f32x16 dp;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            Frag xn;
+            Rows xn;
+            bf16x8 own;
+            if constexpr (!F8) own = x_piece<XT, G>(xb + wave * 32 * ROW, m, own_scale);
 #pragma unroll
             for (int p = 0; p < 2 * NG; ++p) {
                 const int g = p / 2, f = p % 2;
-                const f32x16 d = group_product<G>(xf, wf[f], g);
+                f32x16 d;
+                if constexpr (F8) d = mfma_e4m3(xf.v, group_of<G>(wf[f], g), (f32x16){}, xf.scale, kScaleCode);
+                else d = group_product<G>(xf.v, wf[f], g);
                 if (p == 0 && m + 1 < MT) xn = rows_of(m + 1);
                 if (m || p) {
                     const int pm = p ? m : m - 1, pg = p ? (p - 1) / 2 : NG - 1, pf = (p + 1) % 2;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[pf][pm][r] = __builtin_fmaf(s[pf][pg], dp[r], acc[pf][pm][r]);
                 }
+                if constexpr (!F8)
+                    if (p == 1) {
+                        const u32x4 u = __builtin_bit_cast(u32x4, own);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum[NG == 1 ? 0 : m & 1] = add_pair(u[j], sum[NG == 1 ? 0 : m & 1]);
+                    }
                 __builtin_amdgcn_sched_barrier(0);
                 dp = d;
             }
@@ -932,12 +1042,22 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[1][MT - 1][r] = __builtin_fmaf(s[1][NG - 1], dp[r], acc[1][MT - 1][r]);
+        if constexpr (!F8) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[g]), __float_as_uint(sum[g]), false, false);
+                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, __uint_as_float(both.x) + __uint_as_float(both.y));
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        expand(kb + 1);  // (past the last step: never used)
+        load_codes(min(kb + 2, nkb - 1));
     }
     // the last chunk's missing groups
     for (int slot = (nkb - 1) % CHUNK * NG + NG; slot < 16; ++slot) {
         store_sum((nkb - 1) / CHUNK, slot, 0.0f);
-        store_bias(0, slot, 0);
-        store_bias(1, slot, 0);
+        store_bias((nkb - 1) / CHUNK, 0, slot, 0);
+        store_bias((nkb - 1) / CHUNK, 1, slot, 0);
     }
     barrier_no_fence();
     fold((nkb - 1) / CHUNK);
@@ -951,46 +1071,69 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
 }
 
-template <int XT, int G, bool GATED>
-hipError_t launch_many(const LinearArgs &a, hipStream_t s) {
-    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8;
-    const int total = (obs + tiles - 1) / tiles * ((a.t + 127) / 128);
-    hipLaunchKernelGGL((k_linear_many<G, GATED>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
+#ifndef MMT
+#define MMT 4
+#endif
+template <int XT, int G, bool GATED, bool F8>
+hipError_t launch_many_as(const LinearArgs &a, hipStream_t s) {
+    constexpr int MT = MMT;
+    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 32 * MT - 1) / (32 * MT));
+    hipLaunchKernelGGL((k_linear_many<XT, G, GATED, F8, MT>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
     return hipGetLastError();
 }
+template <int XT, int G, bool GATED>
+hipError_t launch_many(const LinearArgs &a, hipStream_t s) {
+    // The e4m3 MFMA adds its 64 products to about 16 bits: enough for outputs
+    // of 8 bits of mantissa or fewer, not for fp32 ones.
+    if constexpr (XT == MOE_E4M3)
+        if (a.out_type != MOE_F32) return launch_many_as<XT, G, GATED, true>(a, s);
+    return launch_many_as<XT, G, GATED, false>(a, s);
+}
 
-#ifndef SPLIT_MT
-#define SPLIT_MT 1
-#define SPLIT_NT 2
-#endif
 template <int XT, int G, bool GATED, int MT, int NT>
-hipError_t launch_split_block(const LinearArgs &a, hipStream_t s) {
+hipError_t launch_split_block(const LinearArgs &a, int W, hipStream_t s) {
     const int nkb = a.k >> 6;
-#ifndef SPW
-#define SPW kMaxWaves
-#endif
-    int W = SPW;
     while (W > 1 && W > nkb) W /= 2;
     const dim3 grid((unsigned)(((a.n + 31) / 32 + NT - 1) / NT), (a.t + 32 * MT - 1) / (32 * MT));
     const size_t lds = (size_t)W * std::max((GATED ? 2 : NT) * 16 * 64 * 4, 2 * 32 * MT * kRowBytes<XT>);
     hipLaunchKernelGGL((k_linear_split<XT, G, GATED, MT, NT>), grid, dim3(64 * W), lds, s, a);
     return hipGetLastError();
 }
+// The smallest block that fits one round of 256 workgroups (a larger one costs
+// each workgroup more time than it saves: 64 x 4096 x 4096 takes 7.7 us in 32 x
+// 32 blocks, 9.4 in 32 x 64, 14.7 in 64 x 64), else 64 x 64 (256 x 4096 x 4096:
+// 16.7 us, against 20.4 in 32 x 64).  From two rounds on, workgroups of 4 waves
+// (512 x 4096 x 4096: 30 us, against 32 with 8).
 template <int XT, int G, bool GATED>
 hipError_t launch_split(const LinearArgs &a, hipStream_t s) {
-    return launch_split_block<XT, G, GATED, SPLIT_MT, GATED ? 1 : SPLIT_NT>(a, s);
+    const long tb = (a.t + 31) / 32, tb2 = (a.t + 63) / 64, nb = (a.n + 31) / 32, nb2 = (a.n + 63) / 64;
+    if constexpr (GATED) {
+        if (tb * nb <= 256) return launch_split_block<XT, G, true, 1, 1>(a, kMaxWaves, s);
+        return launch_split_block<XT, G, true, 2, 1>(a, tb2 * nb >= 512 ? 4 : kMaxWaves, s);
+    } else {
+        if (tb * nb <= 256) return launch_split_block<XT, G, false, 1, 1>(a, kMaxWaves, s);
+        if (tb * nb2 <= 256) return launch_split_block<XT, G, false, 1, 2>(a, kMaxWaves, s);
+        return launch_split_block<XT, G, false, 2, 2>(a, tb2 * nb2 >= 512 ? 4 : kMaxWaves, s);
+    }
+}
+
+// Which kernel.  Up to 16 rows the codes' bytes bound the call.  The tiles of
+// k_linear_many pay from about 200 workgroups on (4096 columns: one workgroup
+// a CU 95 us, two 155; k_linear_split takes 0.47 us for the outputs of one).
+#ifndef MANY_WGS
+#define MANY_WGS 200
+#endif
+template <int XT, int G, bool GATED>
+hipError_t launch_any(const LinearArgs &a, hipStream_t s) {
+    if (a.t <= 16) return launch_units<XT, G, GATED>(a, s);
+    const long tiles = GATED ? 4 : 8, blocks = ((a.n + 31) / 32 + tiles - 1) / tiles * ((a.t + 127) / 128);
+    if (blocks >= MANY_WGS) return launch_many<XT, G, GATED>(a, s);
+    return launch_split<XT, G, GATED>(a, s);
 }
 
 template <int XT, int G>
 hipError_t launch_gated(const LinearArgs &a, hipStream_t s) {
-#ifndef UMAX
-#define UMAX 16
-#define MANY_T 1024
-#endif
-    if (a.t <= UMAX) return a.record2 ? launch_units<XT, G, true>(a, s) : launch_units<XT, G, false>(a, s);
-    if constexpr (XT == MOE_BF16)
-        if (a.t >= MANY_T && a.ldx_bytes <= 1 << 24) return a.record2 ? launch_many<XT, G, true>(a, s) : launch_many<XT, G, false>(a, s);
-    return a.record2 ? launch_split<XT, G, true>(a, s) : launch_split<XT, G, false>(a, s);
+    return a.record2 ? launch_any<XT, G, true>(a, s) : launch_any<XT, G, false>(a, s);
 }
 
 template <int XT>
