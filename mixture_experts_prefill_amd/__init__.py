@@ -441,20 +441,27 @@ _ROW_TYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.float8_e4m3fn: E4M
 _BLOCK_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
 
 
-def _row_args(x: torch.Tensor, t: int, width: int, what: str):
-    """(pointer, type, row stride) of a t x width row tensor."""
-    if x.dim() != 2 or x.shape[0] != t or x.shape[1] != width:
-        raise ValueError(f"{what} must be a [{t}, {width}] tensor, not {list(x.shape)}")
+def _row_args(x: torch.Tensor, t: int, width: int, dev: int, what: str):
+    """(pointer, type, row stride) of a t x width row tensor on GPU `dev`."""
+    shape = x.shape
+    if len(shape) != 2 or shape[0] != t or shape[1] != width:
+        raise ValueError(f"{what} must be a [{t}, {width}] tensor, not {list(shape)}")
     kind = _ROW_TYPES.get(x.dtype)
     if kind is None:
         raise ValueError(f"{what} must be bfloat16, float32 or float8_e4m3fn, not {x.dtype}")
     ld, step = x.stride()
-    if (step != 1 and width > 1) or (ld < width and t > 1):
-        raise ValueError(f"{what} needs a contiguous last dimension and rows that do not overlap")
-    return x.data_ptr(), kind, ld if t > 1 and ld >= width else width + -width % 16
+    if step != 1 and width > 1:
+        raise ValueError(f"{what} needs a contiguous last dimension")
+    if t == 1:
+        ld = width + -width % 16  # one row: any stride will do
+    elif ld < width:
+        raise ValueError(f"{what} needs rows that do not overlap")
+    if x.get_device() != dev or dev < 0:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    return x.data_ptr(), kind, ld
 
 
-def _scale_args(scale: Optional[torch.Tensor], t: int, width: int, what: str):
+def _scale_args(scale: Optional[torch.Tensor], t: int, width: int, dev: int, what: str):
     """(pointer, kind) of the scales of 8-bit rows."""
     if scale is None:
         return None, SCALE_NONE
@@ -464,30 +471,25 @@ def _scale_args(scale: Optional[torch.Tensor], t: int, width: int, what: str):
         kind, n = SCALE_BLOCK, t * (width // 32)
     else:
         raise ValueError(f"{what} must be float32 (one a row) or uint8 / float8_e8m0fnu (one per 32 columns)")
-    if scale.numel() != n or not scale.is_contiguous():
+    return _flat(scale, n, dev, what), kind
+
+
+def _flat(x: torch.Tensor, n: int, dev: int, what: str) -> int:
+    """The pointer of n contiguous values on GPU `dev`."""
+    if x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {n} values")
-    return scale.data_ptr(), kind
+    if x.get_device() != dev:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    return x.data_ptr()
 
 
-def _launch_device(*tensors: Optional[torch.Tensor]) -> torch.device:
-    """The one GPU that all the tensors are on."""
-    dev = None
-    for x in tensors:
-        if x is None:
-            continue
-        if not x.is_cuda or (dev is not None and x.device != dev):
-            raise ValueError("tensors passed to libmoe must be on one GPU")
-        dev = x.device
-    return dev
-
-
-def _call_on(dev: torch.device, stream, fn, *args) -> None:
-    """fn(*args, stream) with `dev` current, on the given stream or dev's current one."""
-    if dev.index != torch.cuda.current_device():
+def _call_on(dev: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with GPU `dev` current, on the given stream or dev's current one."""
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call_on(dev, stream, fn, *args)
     # the raw handle of the current stream: torch.cuda.current_stream() builds a Python object in 2.5 us
-    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status != 0:
         _check(status)
 
@@ -498,9 +500,12 @@ def moe_matrix_layout_make(n: int, k: int, group: int) -> moe_matrix_layout:
     return out
 
 
-def _check_record(record: torch.Tensor, layout: moe_matrix_layout) -> int:
+def _record(record: torch.Tensor, layout: moe_matrix_layout, dev: int) -> int:
+    """The pointer of a record of this layout on GPU `dev`."""
     if not record.is_contiguous() or record.numel() * record.element_size() < layout.bytes:
         raise ValueError(f"a record of this layout is {layout.bytes} contiguous bytes")
+    if record.get_device() != dev:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
     return record.data_ptr()
 
 
@@ -508,13 +513,12 @@ def moe_linear(x: torch.Tensor, layout: moe_matrix_layout, record: torch.Tensor,
                x_scale: Optional[torch.Tensor] = None, accumulate: int = 0, stream=None) -> None:
     """out [t, n] (bf16 or fp32) (+)= x [t, k] times the 4-bit matrix; x bf16, or
     e4m3 with x_scale fp32 [t] or uint8 / float8_e8m0fnu [t, k/32]."""
-    dev = _launch_device(x, record, out, x_scale)
-    t = x.shape[0]
-    xp, xt, ldx = _row_args(x, t, layout.k, "x")
-    op, ot, ldo = _row_args(out, t, layout.n, "out")
-    sp, sk = _scale_args(x_scale, t, layout.k, "x_scale")
-    _call_on(dev, stream, lib().moe_linear, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
-             _check_record(record, layout), op, ot, ldo, accumulate)
+    dev, t, n, k = x.get_device(), x.shape[0], layout.n, layout.k
+    xp, xt, ldx = _row_args(x, t, k, dev, "x")
+    op, ot, ldo = _row_args(out, t, n, dev, "out")
+    sp, sk = _scale_args(x_scale, t, k, dev, "x_scale")
+    _call_on(dev, stream, (_lib or lib()).moe_linear, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
+             _record(record, layout, dev), op, ot, ldo, accumulate)
 
 
 def moe_linear_gated(x: torch.Tensor, layout: moe_matrix_layout, gate_record: torch.Tensor, up_record: torch.Tensor,
@@ -522,16 +526,15 @@ def moe_linear_gated(x: torch.Tensor, layout: moe_matrix_layout, gate_record: to
                      out_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """out [t, n] = silu(x Wg^T) * (x Wu^T); out bf16, fp32, or e4m3 with
     out_scale uint8 / float8_e8m0fnu [t, n/32]; x as for moe_linear."""
-    dev = _launch_device(x, gate_record, up_record, out, x_scale, out_scale)
-    t = x.shape[0]
-    xp, xt, ldx = _row_args(x, t, layout.k, "x")
-    op, ot, ldo = _row_args(out, t, layout.n, "out")
-    sp, sk = _scale_args(x_scale, t, layout.k, "x_scale")
-    qp, qk = _scale_args(out_scale, t, layout.n, "out_scale")
+    dev, t, n, k = x.get_device(), x.shape[0], layout.n, layout.k
+    xp, xt, ldx = _row_args(x, t, k, dev, "x")
+    op, ot, ldo = _row_args(out, t, n, dev, "out")
+    sp, sk = _scale_args(x_scale, t, k, dev, "x_scale")
+    qp, qk = _scale_args(out_scale, t, n, dev, "out_scale")
     if qk == SCALE_ROW:
         raise ValueError("out_scale is one byte per 32 columns")
-    _call_on(dev, stream, lib().moe_linear_gated, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
-             _check_record(gate_record, layout), _check_record(up_record, layout), op, ot, ldo, qp)
+    _call_on(dev, stream, (_lib or lib()).moe_linear_gated, xp, xt, ldx, sp, sk, t, ctypes.byref(layout),
+             _record(gate_record, layout, dev), _record(up_record, layout, dev), op, ot, ldo, qp)
 
 
 def moe_residual_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -541,24 +544,28 @@ def moe_residual_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual
     """residual_out = x + residual (rounded to its type) and the RMS norm of it
     as bf16 rows `out`, as e4m3 rows `codes` with `scale` (fp32 [t], or uint8 /
     float8_e8m0fnu [t, h/32]), or both; without a residual the norm of x."""
-    dev = _launch_device(x, gamma, residual, residual_out, out, codes, scale)
+    dev = x.get_device()
     t, h = x.shape
-    xp, xt, ldx = _row_args(x, t, h, "x")
-    rp, rt, ldr = (None, BF16, 0) if residual is None else _row_args(residual, t, h, "residual")
-    rop = None
+    xp, xt, ldx = _row_args(x, t, h, dev, "x")
+    rp, rt, ldr, rop = None, BF16, 0, None
+    if residual is not None:
+        rp, rt, ldr = _row_args(residual, t, h, dev, "residual")
     if residual_out is not None:
-        rop, rot, ldro = _row_args(residual_out, t, h, "residual_out")
-        if residual is not None and (rot, ldro) != (rt, ldr):
+        rop, rot, ldro = _row_args(residual_out, t, h, dev, "residual_out")
+        if residual is not None and (rot != rt or ldro != ldr):
             raise ValueError("residual_out must have the residual's type and row stride")
-    op, ot, ldo = (None, BF16, 0) if out is None else _row_args(out, t, h, "out")
-    cp, ct, ldc = (None, E4M3, 0) if codes is None else _row_args(codes, t, h, "codes")
-    sp, sk = _scale_args(scale, t, h, "scale")
-    if ot != BF16 or ct != E4M3 or (codes is None) != (scale is None):
+    op, ot, ldo, cp, ct, ldc = None, BF16, 0, None, E4M3, 0
+    if out is not None:
+        op, ot, ldo = _row_args(out, t, h, dev, "out")
+    if codes is not None:
+        cp, ct, ldc = _row_args(codes, t, h, dev, "codes")
+    sp, sk = _scale_args(scale, t, h, dev, "scale")
+    if ot != BF16 or ct != E4M3 or (cp is None) != (sp is None):
         raise ValueError("out is bfloat16, codes are float8_e4m3fn and have a scale")
-    if gamma.dtype != torch.float32 or gamma.numel() != h or not gamma.is_contiguous():
-        raise ValueError(f"gamma must be contiguous float32 [{h}]")
-    _call_on(dev, stream, lib().moe_residual_norm, xp, xt, ldx, rp, rop, rt, ldr, gamma.data_ptr(), eps, t, h, op, ldo,
-             cp, ldc, sp, sk)
+    if gamma.dtype != torch.float32:
+        raise ValueError("gamma must be float32")
+    _call_on(dev, stream, (_lib or lib()).moe_residual_norm, xp, xt, ldx, rp, rop, rt, ldr,
+             _flat(gamma, h, dev, "gamma"), eps, t, h, op, ldo, cp, ldc, sp, sk)
 
 
 def moe_ring_plan_debug(offsets, resident, n_slots: int = 64, group: int = 8):

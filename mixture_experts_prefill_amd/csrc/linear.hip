@@ -682,26 +682,43 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
     load(b0, k0);  // in bounds for a wave without a step too
     if constexpr (STAGED) {
         const int pieces = a.k >> 3, rows = min(a.t - t0, 4 * NR);
-        for (int r = 0; r < rows; ++r) {
-            const uint8_t *src = a.x + (size_t)(t0 + r) * a.ldx_bytes;
-            const uint8_t *sc = static_cast<const uint8_t *>(a.x_scale) + (size_t)(t0 + r) * (a.k >> 5);
+        constexpr int BATCH = 2;  // rows whose loads are issued together
+        for (int r0 = 0; r0 < rows; r0 += BATCH)
             for (int c = threadIdx.x; c < pieces; c += blockDim.x) {
-                u32x4 v;
-                if constexpr (XT == MOE_BF16) {
-                    v = load16(src + c * 16);
-                } else {
-                    const uint32_t scale = block_scales ? load1(sc + (c >> 2)) : 127u;
-                    v = __builtin_bit_cast(u32x4, e4m3_bf16(load8(src + c * 8), __uint_as_float(scale << 23)));
+                u32x4 v[BATCH];
+                uint32_t scale[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = t0 + min(r0 + i, rows - 1);  // past the last row: it again, to its own place
+                    const uint8_t *src = a.x + (size_t)r * a.ldx_bytes;
+                    if constexpr (XT == MOE_BF16) {
+                        v[i] = load16(src + c * 16);
+                    } else {
+                        const u32x2 e = load8(src + c * 8);
+                        v[i] = (u32x4){e.x, e.y, 0, 0};
+                        const uint8_t *sc = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : src;
+                        scale[i] = load1(sc + (c >> 2));
+                    }
                 }
-                *reinterpret_cast<u32x4 *>(staged_base + r * stride + c * 16) = permute8(v);
-                float sum = 0.0f;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xffff0000u);
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = min(r0 + i, rows - 1);
+                    if constexpr (XT == MOE_E4M3)
+                        v[i] = __builtin_bit_cast(u32x4, e4m3_bf16((u32x2){v[i].x, v[i].y},
+                                                                   __uint_as_float((block_scales ? scale[i] : 127u) << 23)));
+                    *reinterpret_cast<u32x4 *>(staged_base + r * stride + c * 16) = permute8(v[i]);
+                    float sum = 0.0f;
 #pragma unroll
-                for (int off = 1; off < G / 8; off *= 2) sum += __shfl_xor(sum, off, 64);
-                if (c % (G / 8) == 0) sums[(c / (G / 8)) * (4 * NR) + r] = sum;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t u = v[i][j];
+                        sum += __uint_as_float(u << 16) + __uint_as_float(u & 0xffff0000u);
+                    }
+#pragma unroll
+                    for (int off = 1; off < G / 8; off *= 2) sum += __shfl_xor(sum, off, 64);
+                    if (c % (G / 8) == 0) sums[(c / (G / 8)) * (4 * NR) + r] = sum;
+                }
             }
-        }
         // rows past the last: no garbage in the sums (their outputs are not stored)
         for (int i = threadIdx.x; i < (nkb * NG) * (4 * NR); i += blockDim.x)
             if (i % (4 * NR) >= rows) sums[i] = 0.0f;
@@ -751,7 +768,11 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
 // output's block needs two units), and as many waves to split K as bring the
 // launch to about kUnitWaves.
 constexpr int kUnitWaves = 8192;
-constexpr size_t kStagedBytes = 64 * 1024;  // most LDS with staged rows
+// Most bytes of staged rows, in a launch of few workgroups and of many: more
+// take longer to stage than they save (one row: 4096 x 8192 7.6 -> 7.1 us, the
+// gated 8192 x 4096 11.7 -> 9.5; four: 32768 x 4096 17.0 -> 15.1 us, but 4096 x
+// 4096 4.9 -> 5.4; eight: 100003 x 2048 27.7 -> 29.6).
+constexpr size_t kStagedFew = 20 * 1024, kStagedMost = 40 * 1024;
 
 template <int XT, int G, bool GATED, int MT, int NR>
 hipError_t launch_units_mt(const LinearArgs &a, hipStream_t s) {
@@ -764,9 +785,9 @@ hipError_t launch_units_mt(const LinearArgs &a, hipStream_t s) {
     const dim3 grid(wgs, (a.t + 16 * MT - 1) / (16 * MT)), block(64 * W);
     const int NU = (GATED ? 2 : 1) * (pair ? 2 : 1);
     const size_t lds = W > 1 ? (size_t)W * NU * NR * 64 * 4 : 0;
-    if constexpr (MT == 1) {
+    if constexpr (NR == 1) {
         const size_t staged = (size_t)(a.k / G) * 4 * NR * 4 + (size_t)a.t * (a.k * 2 + 16);
-        if (lds + staged <= kStagedBytes) {
+        if (staged <= (wgs >= 512 ? kStagedMost : kStagedFew)) {
             if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 2, true>), grid, block, lds + staged, s, a);
             else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 1, true>), grid, block, lds + staged, s, a);
             return hipGetLastError();
@@ -1071,12 +1092,9 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
         }
 }
 
-#ifndef MMT
-#define MMT 4
-#endif
 template <int XT, int G, bool GATED, bool F8>
 hipError_t launch_many_as(const LinearArgs &a, hipStream_t s) {
-    constexpr int MT = MMT;
+    constexpr int MT = 4;
     const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 32 * MT - 1) / (32 * MT));
     hipLaunchKernelGGL((k_linear_many<XT, G, GATED, F8, MT>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -1101,33 +1119,31 @@ hipError_t launch_split_block(const LinearArgs &a, int W, hipStream_t s) {
 }
 // The smallest block that fits one round of 256 workgroups (a larger one costs
 // each workgroup more time than it saves: 64 x 4096 x 4096 takes 7.7 us in 32 x
-// 32 blocks, 9.4 in 32 x 64, 14.7 in 64 x 64), else 64 x 64 (256 x 4096 x 4096:
-// 16.7 us, against 20.4 in 32 x 64).  From two rounds on, workgroups of 4 waves
-// (512 x 4096 x 4096: 30 us, against 32 with 8).
+// 32 blocks, 9.4 in 32 x 64, 14.7 in 64 x 64), else 32 x 64 or 64 x 64; a 64-row
+// block takes 1.75 times a 32-row one's time.  From two rounds on, workgroups of
+// 4 waves (512 x 4096 x 4096: 30 us, against 32 with 8).
 template <int XT, int G, bool GATED>
 hipError_t launch_split(const LinearArgs &a, hipStream_t s) {
-    const long tb = (a.t + 31) / 32, tb2 = (a.t + 63) / 64, nb = (a.n + 31) / 32, nb2 = (a.n + 63) / 64;
-    if constexpr (GATED) {
-        if (tb * nb <= 256) return launch_split_block<XT, G, true, 1, 1>(a, kMaxWaves, s);
-        return launch_split_block<XT, G, true, 2, 1>(a, tb2 * nb >= 512 ? 4 : kMaxWaves, s);
-    } else {
-        if (tb * nb <= 256) return launch_split_block<XT, G, false, 1, 1>(a, kMaxWaves, s);
-        if (tb * nb2 <= 256) return launch_split_block<XT, G, false, 1, 2>(a, kMaxWaves, s);
-        return launch_split_block<XT, G, false, 2, 2>(a, tb2 * nb2 >= 512 ? 4 : kMaxWaves, s);
-    }
+    const long tb = (a.t + 31) / 32, tb2 = (a.t + 63) / 64, nb = (a.n + 31) / 32, nb2 = GATED ? nb : (a.n + 63) / 64;
+    constexpr int NT = GATED ? 1 : 2;
+    if (tb * nb <= 256) return launch_split_block<XT, G, GATED, 1, 1>(a, kMaxWaves, s);
+    const bool tall = tb * nb2 > 256 && 7 * tb2 <= 4 * tb;
+    const int W = (tall ? tb2 : tb) * nb2 >= 512 ? 4 : kMaxWaves;
+    return tall ? launch_split_block<XT, G, GATED, 2, NT>(a, W, s) : launch_split_block<XT, G, GATED, 1, NT>(a, W, s);
 }
 
-// Which kernel.  Up to 16 rows the codes' bytes bound the call.  The tiles of
-// k_linear_many pay from about 200 workgroups on (4096 columns: one workgroup
-// a CU 95 us, two 155; k_linear_split takes 0.47 us for the outputs of one).
-#ifndef MANY_WGS
-#define MANY_WGS 200
-#endif
+// Which kernel.  Up to 16 rows the codes' bytes bound the call.  The 128-row
+// tiles of k_linear_many pay from about 200 workgroups on (2048 x 4096 x 4096,
+// 256 of them: 99 us, against 125 split; 1024 x 4096 x 4096, 128: 95 against
+// 58), and if half of their rows are live (80 x 100003 x 2048: 82 us against
+// 91; 64 rows: 78 against 63).
+constexpr long kManyWorkgroups = 200;
+constexpr int kManyRows = 65;
 template <int XT, int G, bool GATED>
 hipError_t launch_any(const LinearArgs &a, hipStream_t s) {
     if (a.t <= 16) return launch_units<XT, G, GATED>(a, s);
     const long tiles = GATED ? 4 : 8, blocks = ((a.n + 31) / 32 + tiles - 1) / tiles * ((a.t + 127) / 128);
-    if (blocks >= MANY_WGS) return launch_many<XT, G, GATED>(a, s);
+    if (blocks >= kManyWorkgroups && a.t >= kManyRows) return launch_many<XT, G, GATED>(a, s);
     return launch_split<XT, G, GATED>(a, s);
 }
 

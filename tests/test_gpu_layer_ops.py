@@ -191,6 +191,92 @@ def test_linear_large(centred):
         assert bool(((alone - out[pick]).double().cpu().abs() <= 2 * err).all())
 
 
+# at least 200 tiles of 128 rows x 256 outputs (128 when gated), the long chunks' kernel: row counts and widths
+# that end inside a tile, one step of K, part of a 16-group chunk, whole chunks and more
+@pytest.mark.parametrize("group", [64, 32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,n,k", [(65, 51200, 64), (100, 51300, 320), (700, 9000, 576), (1300, 4600, 1024),
+                                   (4096, 1700, 1088), (4000, 1800, 2112)])
+def test_long_chunk(t, n, k, kind, group):
+    m = ref.Matrix(n, k, group, 11)
+    dm = device_matrix(m)
+    x, s, d = rows(t, k, 11, kind)
+    g = torch.Generator().manual_seed(t)
+    pick = sorted({0, 1, 31, 32, 63, t - 1, t - 2, t - 33} | set(torch.randint(0, t, (20,), generator=g).tolist()))
+    y, err = m.product(d[pick])
+    for dtype in (F32, BF16):
+        e = err + ref.e4m3_product_error(m, d[pick]) if kind != "bf16" and dtype == BF16 else err
+        buf = torch.full((t + 2, n + 3), GUARD, dtype=dtype, device="cuda")
+        dm.linear(x, s, out=buf[1:t + 1, :n])
+        out = buf[1:t + 1, :n]
+        ref.check_rounded(out[pick], y, e, dtype, (t, n, k, kind, group, dtype))
+        assert bool((buf[0] == GUARD).all() and (buf[-1] == GUARD).all() and (buf[:, n:] == GUARD).all())
+        if dtype == BF16:
+            # rounding to bf16: at most half a step each, evenly spread in it; the e4m3 matrix core adds 2^-12 at most
+            d2 = out[pick].double().cpu() - y
+            assert float(d2.norm() / y.norm()) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -12
+        # no row is left out or doubled: the sum over rows is that of the products
+        want = torch.stack([d.sum(0)]) @ m.values().t()
+        total = out.double().sum(0).cpu()
+        bound = t * (e.max() + ref.HALF[dtype] * y.abs().max() * 2)
+        assert bool(((total - want[0]).abs() <= bound).all())
+    base = torch.randn(t, n, generator=g).to(BF16)
+    out = base.cuda()
+    dm.linear(x, s, out=out, accumulate=1)
+    b = base[pick].double()
+    e = err + (ref.e4m3_product_error(m, d[pick]) if kind != "bf16" else 0)
+    ref.check_rounded(out[pick], y + b, e + ref.U32 * (y.abs() + b.abs()), BF16, "accumulate")
+
+
+@pytest.mark.parametrize("group", [64, 32])
+@pytest.mark.parametrize("kind", ["bf16", "row", "block"])
+@pytest.mark.parametrize("t,n,k", [(70, 25600, 128), (1000, 3300, 704), (4096, 896, 1088)])
+def test_long_chunk_gated(t, n, k, kind, group):
+    g, u = ref.Matrix(n - n % 32, k, group, 1), ref.Matrix(n - n % 32, k, group, 2)
+    n = g.n
+    dg, du = device_matrix(g), device_matrix(u)
+    x, s, d = rows(t, k, 12, kind)
+    gen = torch.Generator().manual_seed(t)
+    pick = sorted({0, 31, 32, t - 1} | set(torch.randint(0, t, (12,), generator=gen).tolist()))
+    (yg, eg), (yu, eu) = g.product(d[pick]), u.product(d[pick])
+    y, err = ref.gated((yg, eg), (yu, eu))
+    ref.check_rounded(dg.gated(du, x, s, out_dtype=F32)[pick], y, err, F32, (t, n, k, kind, group))
+    if kind != "bf16":
+        y, err = ref.gated((yg, eg + ref.e4m3_product_error(g, d[pick])), (yu, eu + ref.e4m3_product_error(u, d[pick])))
+    ref.check_rounded(dg.gated(du, x, s)[pick], y, err, BF16, (t, n, k, kind, group))
+    codes, scale = dg.gated(du, x, s, out_dtype=E4M3)
+    ref.check_codes(codes.view(torch.uint8)[pick].view(E4M3), scale[pick], y, err, (t, n, k, kind, group))
+
+
+def test_long_chunk_bad_rows_and_bits():
+    """NaN and infinite rows stay alone; the same call gives the same bits, on another stream too."""
+    t, n, k = 4096, 1800, 512
+    m = ref.Matrix(n, k, 64)
+    dm = device_matrix(m)
+    for kind in ("bf16", "block"):
+        x, s, _ = rows(t, k, 13, kind)
+        for dtype in (F32, BF16):
+            want = dm.linear(x, s, out_dtype=dtype)
+            bits = torch.int32 if dtype == F32 else torch.int16
+            side = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            again = torch.empty_like(want)
+            dm.linear(x, s, out=again, stream=side)
+            side.synchronize()
+            assert torch.equal(again.view(bits), want.view(bits))
+            bad = x.clone()
+            if kind == "bf16":
+                bad[77, 5], bad[4095, 70] = float("nan"), float("inf")
+            else:
+                bad.view(torch.uint8)[77, 5] = 0x7F
+                bad.view(torch.uint8)[4095, 70] = 0xFF
+            got = dm.linear(bad, s, out_dtype=dtype)
+            good = torch.ones(t, dtype=torch.bool)
+            good[[77, 4095]] = False
+            assert torch.equal(got[good.cuda()].view(bits), want[good.cuda()].view(bits))
+            assert not bool(torch.isfinite(got[[77, 4095]]).any())
+
+
 def test_same_call_same_bits():
     for t in (1, 20, 200):
         m = ref.Matrix(300, 1024, 64)

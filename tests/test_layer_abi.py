@@ -189,7 +189,7 @@ def test_python_refuses_before_the_library(lib):
     for bad, what in [(x[:, :32], "must be"), (x.half(), "bfloat16"), (x.t(), "must be"),
                       (torch.zeros(64, 2).t(), "contiguous"), (torch.zeros(1, 64).expand(2, 64), "overlap")]:
         with pytest.raises(ValueError, match=what):
-            mep._row_args(bad, 2, 64, "x")
+            mep._row_args(bad, 2, 64, 0, "x")
     for bad in (torch.zeros(3), torch.zeros(2, 2, dtype=torch.float16), torch.zeros(2, 4, dtype=torch.uint8)[:, ::2]):
         with pytest.raises(ValueError):
-            mep._scale_args(bad, 2, 64, "scale")
+            mep._scale_args(bad, 2, 64, 0, "scale")
