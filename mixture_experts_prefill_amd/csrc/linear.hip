@@ -823,8 +823,10 @@ hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
 // the rows of block w.
 //
 // Workgroups go to the 8 XCDs round-robin: XCD x takes the x-th eighth of the
-// (row block, output block) pairs, so its workgroups share rows and codes in
-// its L2.
+// (row block, output block) pairs, listed in bands of 8 row blocks, output
+// block by output block, so that the workgroups of an XCD that run together
+// share both rows and codes in its L2.
+constexpr int kBand = 8;
 template <int XT, int G, bool GATED, bool F8, int MT>
 __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs a) {
     static_assert(!F8 || XT == MOE_E4M3, "e4m3 products are of e4m3 rows");
@@ -842,7 +844,9 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
     const int nblk = (obs + TILES - 1) / TILES, total = nblk * ((a.t + BM - 1) / BM);
     const int share = (total + 7) >> 3, logical = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= share || logical >= total) return;
-    const int t0 = logical / nblk * BM, tile0 = logical % nblk * TILES + wave * (GATED ? 1 : 2);
+    const int band = logical / (kBand * nblk), in_band = logical % (kBand * nblk);
+    const int tall = min(kBand, (a.t + BM - 1) / BM - band * kBand);  // row blocks of the band
+    const int t0 = (band * kBand + in_band % tall) * BM, tile0 = in_band / tall * TILES + wave * (GATED ? 1 : 2);
 
     // The wave's two tiles: code and scale sections of their tile row.  A tile
     // past the matrix is the last one again and stores nothing.
