@@ -540,9 +540,13 @@ moe_status moe_matrix_layout_make(int32_t n, int32_t k, int32_t group, moe_matri
  *   M          [host] layout; record: M->bytes bytes, 16-byte aligned
  *   out        bf16 or fp32 [t][n] (out_type), row stride ldo; accumulate = 0
  *              overwrites, 1 adds (in fp32, one rounding)
- * Products of codes and rows are summed exactly as they are (no weight is
- * rounded): per group, scale * sum(q x) + bias * sum(x), every sum in fp32,
- * so a row's group sums 15 * sum|x| have to stay inside fp32's range.  A row that
+ * No weight is rounded: codes and rows are multiplied as they are, and per
+ * group scale * sum(q x) + bias * sum(x) is added up in fp32, so a row's group
+ * sums 15 * sum|x| have to stay inside fp32's range.  The sums inside a group
+ * are fp32 too, but for long chunks of e4m3 rows with outputs of 8 bits or
+ * fewer (bf16, e4m3), where the matrix core keeps at least 13 bits of a sum's
+ * largest product (about 16 were measured).  8-bit row values below 2^-126 may
+ * count as 0.  A row that
  * holds a NaN or an infinity gives outputs that are not finite; other rows
  * are not affected.
  * Requires 1 <= t <= 4096.  out must not overlap x, its scales or the record.

@@ -9,6 +9,12 @@
 // weight is ever rounded and a code costs about one instruction instead of a
 // multiply-add and a conversion of its own.
 //
+// Three kernels, chosen by launch_any:
+//   k_linear_units   up to 16 rows: bound by the codes' bytes
+//   k_linear_split   more rows, few output tiles: waves split K
+//   k_linear_many    long chunks: 128 x 256 tiles, bound by the matrix core and
+//                    the vector instructions beside it
+//
 // Operand layout.  Rows (tokens) are operand A, weight rows operand B, so a
 // lane of the accumulator holds one output column and its scale and bias are
 // one register each.  A 32 x 64 code tile gives lane L the 32 codes of row
@@ -20,9 +26,13 @@
 // (5 instructions for 8 codes).  A byte 0..15 read as e4m3 is q * 2^-9 (codes
 // 0..7 are the subnormals, 8..15 the first binade, one straight line), so
 // v_cvt_scalef32_pk_bf16_fp8 with 2^9 gives two exact bf16 codes.  8-bit rows
-// become bf16 by the same instruction, block scale included, exactly.  The
-// group sums of x come from the matrix core too, as the product with a matrix
-// of ones, in the accumulator's layout.
+// become bf16 by the same instruction, block scale included, exactly: the bf16
+// MFMA adds its products up to about 1e-7 of their largest (measured), where
+// the e4m3 MFMA, of twice the rate, keeps about 16 bits (2.5e-5); that one
+// serves long chunks whose outputs are rounded to 8 bits or fewer anyway.
+//
+// Times here are medians of a kernel on one otherwise idle MI355X, inputs cold
+// in the caches of the call before; where two stand, both were timed in turn.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -50,16 +60,14 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ u32x4 load16(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL u32x4 *>(reinterpret_cast<uintptr_t>(p));
 }
-__device__ __forceinline__ u32x4 load16_once(const uint8_t *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const GLOBAL u32x4 *>(reinterpret_cast<uintptr_t>(p)));
-}
 __device__ __forceinline__ u32x2 load8(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL u32x2 *>(reinterpret_cast<uintptr_t>(p));
 }
-// A buffer of `bytes` bytes from p on (the same for every lane), and loads from
-// it.  Every offset used here is inside the buffer: the hardware's range check
-// does not cover the scalar offset and is not relied on.
-// (The compiler loses track of that in 64-bit products, and would then loop over the lanes' buffers.)
+// A buffer of `bytes` bytes from p on, and loads from it.  Every offset used
+// here is inside the buffer: the hardware's range check does not cover the
+// scalar offset and is not relied on.  p is the same for every lane, which the
+// compiler loses track of in 64-bit products (it would then loop over the
+// lanes' buffers): readfirstlane says it again.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
     const uint64_t b = reinterpret_cast<uintptr_t>(p);
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
@@ -77,14 +85,8 @@ template <int HINT = 0>
 __device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
     return __builtin_amdgcn_raw_buffer_load_b32(b, lane_offset, offset, HINT);
 }
-__device__ __forceinline__ u32x2 buffer_load8_plain(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, offset, 0));
-}
 __device__ __forceinline__ uint32_t buffer_load1(__amdgpu_buffer_rsrc_t b, uint32_t lane_offset, int offset) {
     return __builtin_amdgcn_raw_buffer_load_b8(b, lane_offset, offset, 0);
-}
-__device__ __forceinline__ uint32_t load4_once(const uint8_t *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const GLOBAL uint32_t *>(reinterpret_cast<uintptr_t>(p)));
 }
 __device__ __forceinline__ uint32_t load1(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL uint8_t *>(reinterpret_cast<uintptr_t>(p));
@@ -340,13 +342,15 @@ __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int co
         if (live && col + SPAN * i < a.n) store_one<GATED>(a, row, col + SPAN * i, v[i]);
 }
 
-// ---------------------------------------------------------------- some hundred rows
+// ---------------------------------------------------------------- 17 rows and more, few output tiles
 
 // Too few output tiles to fill the chip with long-running workgroups, so the
 // waves of a workgroup split the 64-column steps of one output block, 32 MT
 // rows by NT tiles of 32 outputs (gated: one tile of each matrix): wave w
 // takes the w-th run of steps, and the waves' sums meet in LDS, added in wave
-// order.  Waves do not wait for each other before that.
+// order.  Waves do not wait for each other before that.  Bound by latency, two
+// waves a SIMD at the larger blocks: 512 x 2048 outputs of k = 8192 take 30 us,
+// the matrix core busy for a third of them, the vector units for 40%.
 //
 // A wave's rows come by DMA into LDS of its own, 128 (e4m3: 64) adjacent bytes
 // of a row at a time; loaded straight into the operand's lanes, 16 bytes here
@@ -480,16 +484,18 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
     }
 }
 
-// ---------------------------------------------------------------- up to 64 rows
+// ---------------------------------------------------------------- up to 16 rows
 
 // Bound by the weights' bytes: every code is read once, by one wave, and all
 // else is arranged so that enough loads are in flight and few instructions are
 // spent on a code.  The matrix core runs 16x16x32 products (tokens x outputs;
-// a 16-token block costs a quarter of the 32x32 form's time when there are few
-// tokens).  A unit is 16 outputs; a wave owns RH units (of both matrices when
-// gated) for 16 MT rows, and the workgroup's waves split the 64-column steps
-// as above, their sums meeting in LDS in wave order.  The host picks the
-// number of waves (launch_units).
+// a 16-token block costs a quarter of the 32x32 form's time).  A unit is 16
+// outputs; a wave owns RH units (of both matrices when gated) for all rows, and
+// the workgroup's waves deal out the 64-column steps among themselves, wave w
+// taking steps w, w + W, ..; their sums meet in LDS and are added in wave
+// order.  The host picks the number of waves (launch_units_rows).
+// One row: 100003 x 2048 in 19 us, 6.1 TB/s of codes and scales, the rate of a
+// plain read; 4096 x 4096 in 5 us, where launch and latency are most of it.
 //
 // Lane (row or output L % 16, quarter L / 16) of a step: with groups of 64,
 // MFMA i takes columns 16 (L / 16) + 8 i of the 64; with groups of 32, MFMA i
@@ -544,37 +550,30 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-//
 // STAGED: the workgroup first copies its rows to LDS, as bf16, with their
 // group sums.  Loaded from the cache for every step instead, they cost as much
 // of its bandwidth as the codes (a lane needs 32 bytes of rows for 16 of codes
 // a step, and most lanes' are copies): 100003 x 2048, one row, 25.7 -> 21 us.
-template <int XT, int G, bool GATED, int MT, int NR, int RH, bool STAGED>
+template <int XT, int G, bool GATED, int NR, int RH, bool STAGED>
 __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
     constexpr int NM = GATED ? 2 : 1, NU = NM * RH, NG = 64 / G;
-    constexpr int U = MT == 1 && NU == 1 ? 4 : MT <= 2 ? 2 : 1;
-    static_assert(MT == 1 || NR == 4, "several row blocks use every register");
-    static_assert(!STAGED || MT == 1, "one row block is staged");
+    constexpr int U = NU == 1 ? 4 : 2;  // steps loaded together
     extern __shared__ float red[];  // [waves][NU][NR][64]; then the staged sums [K / G][4 NR] and rows
     const int lane = threadIdx.x & 63, q = lane >> 4, row = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
-    const int unit0 = blockIdx.x * RH, t0 = blockIdx.y * 16 * MT;
+    const int unit0 = blockIdx.x * RH;
     const int nkb = a.k >> 6;
     const bool block_scales = a.x_scale_kind == MOE_SCALE_BLOCK;
 
-    const uint8_t *xp[MT], *xs[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = min(t0 + 16 * m + NR * (row >> 2) + min(row & 3, NR - 1), a.t - 1);
-        xp[m] = a.x + (size_t)r * a.ldx_bytes;
-        // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
-        xs[m] = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)r * (a.k >> 5) : xp[m];
-    }
+    const int my_row = min(NR * (row >> 2) + min(row & 3, NR - 1), a.t - 1);
+    const uint8_t *xp = a.x + (size_t)my_row * a.ldx_bytes;
+    // without block scales the row's own bytes are loaded in their place, so that no branch parts the loads
+    const uint8_t *xs = block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)my_row * (a.k >> 5) : xp;
     // Staged rows: 16 bytes of padding shift neighbouring rows' LDS banks.
     const uint32_t stride = a.k * 2 + 16;
     float *sums = red + (W > 1 ? W * NU * NR * 64 : 0);
     uint8_t *staged_base = reinterpret_cast<uint8_t *>(sums + nkb * NG * 4 * NR);
-    const uint8_t *staged = staged_base + min(NR * (row >> 2) + min(row & 3, NR - 1), a.t - 1 - t0) * stride;
+    const uint8_t *staged = staged_base + my_row * stride;
     // Buffers over the code and scale sections of the units' tile row (a pair
     // is one tile; rows are padded to whole tiles): a load is then one scalar
     // offset a step and one lane offset, without 64-bit lane arithmetic.
@@ -596,7 +595,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
     struct Batch {
         u32x2 w[U][NU];
         uint32_t sb[U][NU][NG];
-        URows<XT, G> x[STAGED ? 1 : U][MT];
+        URows<XT, G> x[STAGED ? 1 : U];
     };
     auto load = [&](Batch &b, int k0) {
 #pragma unroll
@@ -605,23 +604,21 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
 #pragma unroll
             for (int f = 0; f < NU; ++f) {
                 if constexpr (G == 64) b.w[u][f] = buffer_load8(wb[f / RH], wo[f % RH], kb * 1024);
-                else b.w[u][f] = (u32x2){buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH], kb * 1024), buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH] + 512, kb * 1024)};
+                else
+                    b.w[u][f] = (u32x2){buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH], kb * 1024),
+                                        buffer_load4<kNonTemporal>(wb[f / RH], wo[f % RH] + 512, kb * 1024)};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) b.sb[u][f][g] = buffer_load4<kNonTemporal>(sb[f / RH], so[f % RH] + g * 128, kb * (128 * NG));
             }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                if (!STAGED) b.x[u][m] = load_unit_rows<XT, G>(xp[m], kb, q, xs[m]);
+            if constexpr (!STAGED) b.x[u] = load_unit_rows<XT, G>(xp, kb, q, xs);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    float acc[NU][MT][NR];
+    float acc[NU][NR];
 #pragma unroll
     for (int f = 0; f < NU; ++f)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) acc[f][m][r] = 0.0f;
+        for (int r = 0; r < NR; ++r) acc[f][r] = 0.0f;
     // Steps past the last (in the last batch) repeat it with scale and bias 0.
     auto compute = [&](const Batch &b, int k0, auto last) {
         const __bf16 o = (__bf16)1.0f;
@@ -629,26 +626,23 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t live = !decltype(last)::value || k0 + u * W < nkb ? ~0u : 0u;
-            UFrag x[MT];
-            f32x4 xsum[MT][NG];
+            UFrag x;
+            f32x4 xsum[NG];
             if constexpr (STAGED) {
                 const int kb = min(k0 + u * W, nkb - 1);
                 const uint8_t *p = staged + (uint32_t)kb * 128 + q * (G == 64 ? 32 : 16);
-                x[0].v[0] = *reinterpret_cast<const bf16x8 *>(p);
-                x[0].v[1] = *reinterpret_cast<const bf16x8 *>(p + (G == 64 ? 16 : 64));
+                x.v[0] = *reinterpret_cast<const bf16x8 *>(p);
+                x.v[1] = *reinterpret_cast<const bf16x8 *>(p + (G == 64 ? 16 : 64));
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) xsum[0][g][r] = sums[(kb * NG + g) * (4 * NR) + NR * q + r];
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (STAGED) break;
-                x[m] = unit_rows<XT, G>(b.x[u][m], block_scales);
+                    for (int r = 0; r < NR; ++r) xsum[g][r] = sums[(kb * NG + g) * (4 * NR) + NR * q + r];
+            } else {
+                x = unit_rows<XT, G>(b.x[u], block_scales);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    xsum[m][g] = mfma16(x[m].v[g], one, (f32x4){});
-                    if (G == 64) xsum[m][g] = mfma16(x[m].v[1], one, xsum[m][g]);
+                    xsum[g] = mfma16(x.v[g], one, (f32x4){});
+                    if (G == 64) xsum[g] = mfma16(x.v[1], one, xsum[g]);
                 }
             }
 #pragma unroll
@@ -664,15 +658,13 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
                     c[g] = NR == 1 ? (float)sb.y : in_f32(sb.y);
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int g = 0; g < NG; ++g) {
+                    f32x4 d = mfma16(x.v[g], g ? w1 : w0, (f32x4){});
+                    if (G == 64) d = mfma16(x.v[1], w1, d);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        f32x4 d = mfma16(x[m].v[g], g ? w1 : w0, (f32x4){});
-                        if (G == 64) d = mfma16(x[m].v[1], w1, d);
-#pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            acc[f][m][r] = __builtin_fmaf(c[g], xsum[m][g][r], __builtin_fmaf(s[g], d[r], acc[f][m][r]));
-                    }
+                    for (int r = 0; r < NR; ++r)
+                        acc[f][r] = __builtin_fmaf(c[g], xsum[g][r], __builtin_fmaf(s[g], d[r], acc[f][r]));
+                }
             }
         }
     };
@@ -681,7 +673,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
     int k0 = wave;
     load(b0, k0);  // in bounds for a wave without a step too
     if constexpr (STAGED) {
-        const int pieces = a.k >> 3, rows = min(a.t - t0, 4 * NR);
+        const int pieces = a.k >> 3, rows = min(a.t, 4 * NR);
         constexpr int BATCH = 2;  // rows whose loads are issued together
         for (int r0 = 0; r0 < rows; r0 += BATCH)
             for (int c = threadIdx.x; c < pieces; c += blockDim.x) {
@@ -689,7 +681,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
                 uint32_t scale[BATCH];
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
-                    const int r = t0 + min(r0 + i, rows - 1);  // past the last row: it again, to its own place
+                    const int r = min(r0 + i, rows - 1);  // past the last row: it again, to its own place
                     const uint8_t *src = a.x + (size_t)r * a.ldx_bytes;
                     if constexpr (XT == MOE_BF16) {
                         v[i] = load16(src + c * 16);
@@ -737,36 +729,28 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
         }
     }
 
+    if (W > 1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (W > 1) {
-            if (m) __syncthreads();
+        for (int f = 0; f < NU; ++f)
 #pragma unroll
-            for (int f = 0; f < NU; ++f)
+            for (int r = 0; r < NR; ++r) red[((wave * NU + f) * NR + r) * 64 + lane] = acc[f][r];
+        __syncthreads();
+    }
 #pragma unroll
-                for (int r = 0; r < NR; ++r) red[((wave * NU + f) * NR + r) * 64 + lane] = acc[f][m][r];
-            __syncthreads();
-        }
+    for (int r = 0; r < NR; ++r) {
+        if (r % W != wave) continue;
+        float v[NU];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            if (r % W != wave) continue;
-            float v[NU];
-#pragma unroll
-            for (int f = 0; f < NU; ++f) {
-                v[f] = acc[f][m][r];
-                if (W > 1) {
-                    v[f] = sum_waves(red + (f * NR + r) * 64 + lane, NU * NR * 64, W);
-                }
-            }
-            store_units<GATED, RH, 16>(a, t0 + 16 * m + NR * q + r, unit0 * 16 + row, v);
-        }
+        for (int f = 0; f < NU; ++f) v[f] = W > 1 ? sum_waves(red + (f * NR + r) * 64 + lane, NU * NR * 64, W) : acc[f][r];
+        store_units<GATED, RH, 16>(a, NR * q + r, unit0 * 16 + row, v);
     }
 }
 
-// How k_linear_units runs a call: 16 outputs a wave unless that leaves more
-// than `kUnitWaves` waves even with one wave to a unit pair (or an 8-bit
-// output's block needs two units), and as many waves to split K as bring the
-// launch to about kUnitWaves.
+// How k_linear_units runs a call.  A wave owns a pair of units where an 8-bit
+// output's block needs both, where there are plenty of units (from 1024 on), and
+// where several rows make the rows' loads and sums worth sharing (5 rows and
+// more, from 257 units on).  As many waves split K as bring the launch to
+// kUnitWaves, which is a full chip (256 CUs x 4 SIMDs x 8 waves).
 constexpr int kUnitWaves = 8192;
 // Most bytes of staged rows, in a launch of few workgroups and of many: more
 // take longer to stage than they save (one row: 4096 x 8192 7.6 -> 7.1 us, the
@@ -774,34 +758,33 @@ constexpr int kUnitWaves = 8192;
 // 4096 4.9 -> 5.4; eight: 100003 x 2048 27.7 -> 29.6).
 constexpr size_t kStagedFew = 20 * 1024, kStagedMost = 40 * 1024;
 
-template <int XT, int G, bool GATED, int MT, int NR>
-hipError_t launch_units_mt(const LinearArgs &a, hipStream_t s) {
+template <int XT, int G, bool GATED, int NR>
+hipError_t launch_units_rows(const LinearArgs &a, hipStream_t s) {
     const int units = (a.n + 15) / 16, nkb = a.k >> 6;
     const bool pair = (GATED && a.out_type == MOE_E4M3) || units >= 1024 || (units > 256 && a.t > 4);
     const int wgs = pair ? (units + 1) / 2 : units;
-    const int most = kMaxWaves;
     int W = 1;
-    while (W < most && W * 2 <= nkb && wgs * W < kUnitWaves) W *= 2;
-    const dim3 grid(wgs, (a.t + 16 * MT - 1) / (16 * MT)), block(64 * W);
+    while (W < kMaxWaves && W * 2 <= nkb && wgs * W < kUnitWaves) W *= 2;
+    const dim3 grid(wgs), block(64 * W);
     const int NU = (GATED ? 2 : 1) * (pair ? 2 : 1);
     const size_t lds = W > 1 ? (size_t)W * NU * NR * 64 * 4 : 0;
     if constexpr (NR == 1) {
         const size_t staged = (size_t)(a.k / G) * 4 * NR * 4 + (size_t)a.t * (a.k * 2 + 16);
         if (staged <= (wgs >= 512 ? kStagedMost : kStagedFew)) {
-            if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 2, true>), grid, block, lds + staged, s, a);
-            else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 1, true>), grid, block, lds + staged, s, a);
+            if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, NR, 2, true>), grid, block, lds + staged, s, a);
+            else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, NR, 1, true>), grid, block, lds + staged, s, a);
             return hipGetLastError();
         }
     }
-    if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 2, false>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, MT, NR, 1, false>), grid, block, lds, s, a);
+    if (pair) hipLaunchKernelGGL((k_linear_units<XT, G, GATED, NR, 2, false>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_linear_units<XT, G, GATED, NR, 1, false>), grid, block, lds, s, a);
     return hipGetLastError();
 }
 template <int XT, int G, bool GATED>
 hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
-    if (a.t <= 4) return launch_units_mt<XT, G, GATED, 1, 1>(a, s);
-    if (a.t <= 8) return launch_units_mt<XT, G, GATED, 1, 2>(a, s);
-    return launch_units_mt<XT, G, GATED, 1, 4>(a, s);
+    if (a.t <= 4) return launch_units_rows<XT, G, GATED, 1>(a, s);
+    if (a.t <= 8) return launch_units_rows<XT, G, GATED, 2>(a, s);
+    return launch_units_rows<XT, G, GATED, 4>(a, s);
 }
 
 // ---------------------------------------------------------------- long chunks
@@ -827,10 +810,10 @@ hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
 // block by output block, so that the workgroups of an XCD that run together
 // share both rows and codes in its L2.
 constexpr int kBand = 8;
-template <int XT, int G, bool GATED, bool F8, int MT>
-__global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs a) {
+template <int XT, int G, bool GATED, bool F8>
+__global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     static_assert(!F8 || XT == MOE_E4M3, "e4m3 products are of e4m3 rows");
-    static_assert(F8 || MT == 4, "the four waves sum a block of rows each, a piece beside each block's products");
+    constexpr int MT = 4;  // blocks of 32 rows; each of the four waves sums one
     constexpr int BM = 32 * MT, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
     constexpr int ROW = kRowBytes<XT>, XBUF = BM * ROW, LOADS = XBUF / 4096, PER = 1024 / ROW;  // a wave's loads, rows of one
     constexpr int SUMS = 3 * BM * 32, BIAS = 2 * 32 * 32;  // of a chunk; BIAS: per wave
@@ -878,13 +861,13 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
     const bool block_scales = XT == MOE_E4M3 && a.x_scale_kind == MOE_SCALE_BLOCK;
     const uint32_t srow = a.k >> 5, scales_at = 2 * XBUF + 2 * SUMS + 8 * BIAS;
     const i32x4 rxs = buffer_rsrc(block_scales ? static_cast<const uint8_t *>(a.x_scale) + (size_t)t0 * srow : a.x);
-    const uint32_t svo = (uint32_t)min(32 * (wave % MT) + (lane >> 1), rows - 1) * srow + (lane & 1);
+    const uint32_t svo = (uint32_t)min(32 * wave + (lane >> 1), rows - 1) * srow + (lane & 1);
     auto load_rows = [&](int kb) {
         const u32x4 o = *offsets;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j)
             dma16(lds_base + (kb & 1) * XBUF + (wave * LOADS + j) * 1024, o[j], rx, (uint32_t)kb * ROW);
-        if (block_scales && (MT == 4 || wave < MT)) dma1(lds_base + scales_at + (kb & 1) * SCALES + wave * 256, svo, rxs, (uint32_t)kb * 2u);
+        if (block_scales) dma1(lds_base + scales_at + (kb & 1) * SCALES + wave * 256, svo, rxs, (uint32_t)kb * 2u);
     };
     if (XT == MOE_E4M3 && !block_scales)
         for (int i = threadIdx.x; i < 2 * SCALES / 4; i += 256) reinterpret_cast<uint32_t *>(smem + scales_at)[i] = kScaleOne;
@@ -908,7 +891,7 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
     // Group sum v of row `row` of block `wave`: its three terms into slot `slot` of the chunk's buffer.
     // (both lane halves write the same).
     auto store_sum = [&](int chunk, int slot, float v) {
-        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * (wave % MT) + row) * 32 + slot * 2;
+        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * wave + row) * 32 + slot * 2;
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
             const uint32_t h = __float_as_uint(v) & 0xffff0000u;
@@ -1016,15 +999,13 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
         // beside the products: piece m with block m's.
         float sum[NG];
         if constexpr (F8) {
-            if (MT == 4 || wave < MT) {
-                const Rows own = rows_of(wave);
-                constexpr int o = 0x38383838;  // 1.0
-                const i32x8 one = {o, o, o, o, o, o, o, o};
+            const Rows own = rows_of(wave);
+            constexpr int o = 0x38383838;  // 1.0
+            const i32x8 one = {o, o, o, o, o, o, o, o};
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    store_sum(kb / CHUNK, (kb % CHUNK) * NG + g,
-                              mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0]);
-            }
+            for (int g = 0; g < NG; ++g)
+                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g,
+                          mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0]);
         } else {
 #pragma unroll
             for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
@@ -1098,9 +1079,8 @@ __global__ void __launch_bounds__(256, MT == 4 ? 2 : 3) k_linear_many(LinearArgs
 
 template <int XT, int G, bool GATED, bool F8>
 hipError_t launch_many_as(const LinearArgs &a, hipStream_t s) {
-    constexpr int MT = 4;
-    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 32 * MT - 1) / (32 * MT));
-    hipLaunchKernelGGL((k_linear_many<XT, G, GATED, F8, MT>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
+    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 127) / 128);
+    hipLaunchKernelGGL((k_linear_many<XT, G, GATED, F8>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 template <int XT, int G, bool GATED>
