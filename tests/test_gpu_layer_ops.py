@@ -173,6 +173,29 @@ def test_block_scales_span_the_range():
                        device_matrix(m).linear(c.cuda(), s.cuda(), out_dtype=F32))
 
 
+@pytest.mark.parametrize("group", [64, 32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t,n", [(3, 70), (7, 70), (40, 70), (100, 51200)])
+def test_smallest_block_scales(t, n, dtype, group):
+    """Scale bytes from 0 (2^-127) on.  A row value below 2^-126 may count as 0,
+    and so may a sum: at most k + k / group + 16 sums of each output."""
+    k = 192
+    m = ref.Matrix(n, k, group, seed=3)
+    g = torch.Generator().manual_seed(77)
+    c = torch.randint(0, 256, (t, k), generator=g, dtype=torch.uint8)
+    c[(c & 0x7f) == 0x7f] = 0x3a                                      # no NaN
+    c = c.view(torch.float8_e4m3fn)
+    s = torch.randint(0, 13, (t, k // 32), generator=g, dtype=torch.uint8)
+    s[0] = 0
+    d = c.double() * torch.exp2(s.double() - 127).repeat_interleave(32, 1)
+    y, err = m.product(d)
+    reach = (15 * m.s.double() + m.b.double().abs()).repeat_interleave(group, 1).sum(1)
+    err = err + 2.0 ** -126 * (reach + k + k // group + 16)[None, :]
+    if n == 51200 and dtype == BF16:
+        err = err + ref.e4m3_product_error(m, d)
+    ref.check_rounded(device_matrix(m).linear(c.cuda(), s.cuda(), out_dtype=dtype), y, err, dtype, "small scales")
+
+
 @pytest.mark.parametrize("centred", [True, False])
 def test_linear_large(centred):
     """A full chunk, checked on rows at both ends and in between (row sums against a 64-bit product)."""
