@@ -52,6 +52,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
@@ -305,6 +306,11 @@ __device__ __forceinline__ void store_one(const LinearArgs &a, int row, int col,
     }
 }
 
+// The row's own scale, 1 without one.
+__device__ __forceinline__ float row_scale(const LinearArgs &a, int row) {
+    return a.x_scale_kind == MOE_SCALE_ROW ? static_cast<const float *>(a.x_scale)[min(row, a.t - 1)] : 1.0f;
+}
+
 // RH finished outputs of one row, columns col + (32 / RH) i (gated: then the
 // RH of the second matrix).  All lanes of a wave call it together; the 32 / RH
 // lanes of one row are adjacent, and together they hold 32 adjacent outputs,
@@ -312,11 +318,6 @@ __device__ __forceinline__ void store_one(const LinearArgs &a, int row, int col,
 template <bool GATED, int RH, int SPAN = 32 / RH>
 __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int col, float *v) {
     const bool live = row < a.t;
-    if (a.x_scale_kind == MOE_SCALE_ROW) {
-        const float s = static_cast<const float *>(a.x_scale)[min(row, a.t - 1)];
-#pragma unroll
-        for (int i = 0; i < (GATED ? 2 : 1) * RH; ++i) v[i] *= s;
-    }
     if (GATED) {
 #pragma unroll
         for (int i = 0; i < RH; ++i) v[i] = silu_mul(v[i], v[RH + i]);
@@ -476,10 +477,12 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
             for (int r = 0; r < 16; ++r) red[((wave * NW + f) * 16 + r) * 64 + lane] = acc[f][m][r];
         __syncthreads();
         for (int r = wave; r < 16; r += W) {
+            const int to = t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3);
+            const float scale = row_scale(a, to);
             float v[NW];
 #pragma unroll
-            for (int f = 0; f < NW; ++f) v[f] = sum_waves(red + (f * 16 + r) * 64 + lane, NW * 16 * 64, W);
-            store_units<GATED, NT, 32>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), ob * 32 + row, v);
+            for (int f = 0; f < NW; ++f) v[f] = scale * sum_waves(red + (f * 16 + r) * 64 + lane, NW * 16 * 64, W);
+            store_units<GATED, NT, 32>(a, to, ob * 32 + row, v);
         }
     }
 }
@@ -739,9 +742,10 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_units(LinearArgs a) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         if (r % W != wave) continue;
+        const float scale = row_scale(a, NR * q + r);
         float v[NU];
 #pragma unroll
-        for (int f = 0; f < NU; ++f) v[f] = W > 1 ? sum_waves(red + (f * NR + r) * 64 + lane, NU * NR * 64, W) : acc[f][r];
+        for (int f = 0; f < NU; ++f) v[f] = scale * (W > 1 ? sum_waves(red + (f * NR + r) * 64 + lane, NU * NR * 64, W) : acc[f][r]);
         store_units<GATED, RH, 16>(a, NR * q + r, unit0 * 16 + row, v);
     }
 }
@@ -814,11 +818,13 @@ template <int XT, int G, bool GATED, bool F8>
 __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     static_assert(!F8 || XT == MOE_E4M3, "e4m3 products are of e4m3 rows");
     constexpr int MT = 4;  // blocks of 32 rows; each of the four waves sums one
+    constexpr int NM = GATED ? 2 : 1;
     constexpr int BM = 32 * MT, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
     constexpr int ROW = kRowBytes<XT>, XBUF = BM * ROW, LOADS = XBUF / 4096, PER = 1024 / ROW;  // a wave's loads, rows of one
     constexpr int SUMS = 3 * BM * 32, BIAS = 2 * 32 * 32;  // of a chunk; BIAS: per wave
     constexpr int SCALES = XT == MOE_E4M3 ? BM * 8 : 0;     // block scales of a step: u32 [BM][2]
     __shared__ __align__(128) uint8_t smem[2 * XBUF + 2 * SUMS + 8 * BIAS + 2 * SCALES + 256 * 16];
+    __shared__ __align__(16) float row_scales[XT == MOE_E4M3 ? BM : 4];
     const uint32_t lds_base = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(smem));
     const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -832,15 +838,21 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     const int t0 = (band * kBand + in_band % tall) * BM, tile0 = in_band / tall * TILES + wave * (GATED ? 1 : 2);
 
     // The wave's two tiles: code and scale sections of their tile row.  A tile
-    // past the matrix is the last one again and stores nothing.
-    __amdgpu_buffer_rsrc_t wb[2], sb[2];
+    // past the matrix is the last one again and stores nothing.  Gated: one of
+    // each matrix, lane row's output is column `row` of both.  Else the tiles'
+    // 64 outputs are dealt out in pairs, 2 row and 2 row + 1 to lane row, which
+    // it stores together.
+    __amdgpu_buffer_rsrc_t wb[NM], sb[NM];
+    const int tile = min(tile0, obs - 1), next = GATED ? 0 : min(tile0 + 1, obs - 1) - tile;
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const uint8_t *rec = GATED && f ? a.record2 : a.record;
-        const int tile = GATED ? tile0 : tile0 + f;
-        wb[f] = buffer(rec + a.w + (size_t)min(tile, obs - 1) * nkb * 1024, nkb * 1024);
-        sb[f] = buffer(rec + a.sb + (size_t)min(tile, obs - 1) * nkb * (128 * NG), nkb * (128 * NG));
+    for (int f = 0; f < NM; ++f) {
+        const uint8_t *rec = f ? a.record2 : a.record;
+        wb[f] = buffer(rec + a.w + (size_t)tile * nkb * 1024, (1 + next) * nkb * 1024);
+        sb[f] = buffer(rec + a.sb + (size_t)tile * nkb * (128 * NG), (1 + next) * nkb * (128 * NG));
     }
+    const int pair = 2 * row % 32, of = GATED ? 0 : row / 16 * next * nkb;  // row in its tile, its tile's first step
+    const uint32_t wo = GATED ? lane * 16 : of * 1024 + half * 512 + pair * 16;
+    const uint32_t so = GATED ? row * 4 : of * (128 * NG) + pair * 4;
     // DMA of rows: load j brings PER rows; lane s writes bytes 16 s of them, a
     // part of row PER j + s / (64 / PER).  Rows past the last repeat it.  Block
     // scales: one load a wave, lane s those of row s / 2, block s % 2, as words.
@@ -869,6 +881,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
             dma16(lds_base + (kb & 1) * XBUF + (wave * LOADS + j) * 1024, o[j], rx, (uint32_t)kb * ROW);
         if (block_scales) dma1(lds_base + scales_at + (kb & 1) * SCALES + wave * 256, svo, rxs, (uint32_t)kb * 2u);
     };
+    if (XT == MOE_E4M3 && threadIdx.x < BM) row_scales[threadIdx.x] = row_scale(a, t0 + threadIdx.x);
     if (XT == MOE_E4M3 && !block_scales)
         for (int i = threadIdx.x; i < 2 * SCALES / 4; i += 256) reinterpret_cast<uint32_t *>(smem + scales_at)[i] = kScaleOne;
     u32x4 w[2];
@@ -876,9 +889,10 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     auto load_codes = [&](int kb) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            w[f] = buffer_load16(wb[f], lane * 16, kb * 1024);
+            w[f] = buffer_load16(wb[f % NM], wo + (GATED ? 0 : f * 16), kb * 1024);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) sv[f][g] = buffer_load4(sb[f], row * 4 + g * 128, kb * (128 * NG));
+            for (int g = 0; g < NG; ++g)
+                sv[f][g] = buffer_load4(sb[f % NM], so + (GATED ? 0 : f * 4) + g * 128, kb * (128 * NG));
         }
     };
     const uint32_t x_at = lds_base + row * ROW + (F8 ? part_at<XT>(half, row) : piece_at<XT, G>(row, half));
@@ -1016,6 +1030,9 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
             own_scale[1] = G == 64 ? own_scale[0] : __uint_as_float(xsb[wave * 64 + 1] << 23);
         }
         // Products in order (block, group, tile); each one's multiply-adds run beside the next one's MFMAs.
+        // The next block's rows are read meanwhile; bf16 operands of groups of 32 group by group, each into the
+        // registers of the group just used (with registers of their own the compiler spills to memory).
+        constexpr bool BY_GROUP = !F8 && G == 32;
         Rows xf = rows_of(0);
         f32x16 dp;
 #pragma unroll
@@ -1029,7 +1046,14 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
                 f32x16 d;
                 if constexpr (F8) d = mfma_e4m3(xf.v, group_of<G>(wf[f], g), (f32x16){}, xf.scale, kScaleCode);
                 else d = group_product<G>(xf.v, wf[f], g);
-                if (p == 0 && m + 1 < MT) xn = rows_of(m + 1);
+                if (!BY_GROUP && p == 0 && m + 1 < MT) xn = rows_of(m + 1);
+                if constexpr (BY_GROUP)
+                    if (f == 1 && m + 1 < MT) {
+                        float scale[2] = {1.0f, 1.0f};
+                        if (XT == MOE_E4M3) scale[g] = __uint_as_float(xsb[(m + 1) * 64 + g] << 23);
+                        xf.v.v[g] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g, scale);
+                        xf.v.v[g + 2] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g + 2, scale);
+                    }
                 if (m || p) {
                     const int pm = p ? m : m - 1, pg = p ? (p - 1) / 2 : NG - 1, pf = (p + 1) % 2;
 #pragma unroll
@@ -1044,7 +1068,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
                 __builtin_amdgcn_sched_barrier(0);
                 dp = d;
             }
-            xf = xn;
+            if constexpr (!BY_GROUP) xf = xn;
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[1][MT - 1][r] = __builtin_fmaf(s[1][NG - 1], dp[r], acc[1][MT - 1][r]);
@@ -1068,13 +1092,46 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     barrier_no_fence();
     fold((nkb - 1) / CHUNK);
 
+    // Outputs: without a test each, from one address a lane, where the block is
+    // whole and its pairs aligned (4096 x 4096 x 4096, e4m3 rows: 122 -> 112 us).
+    auto finish = [&](auto put) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float v[2] = {acc[0][m][r], acc[1][m][r]};
-            store_units<GATED, GATED ? 1 : 2, 32>(a, t0 + 32 * m + 8 * (r >> 2) + 4 * half + (r & 3), tile0 * 32 + row, v);
-        }
+            for (int q = 0; q < 4; ++q) {
+                f32x4 scale = {1.0f, 1.0f, 1.0f, 1.0f};
+                if (XT == MOE_E4M3) scale = *reinterpret_cast<const f32x4 *>(row_scales + 32 * m + 8 * q + 4 * half);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    put(32 * m + 8 * q + r, acc[0][m][4 * q + r] * scale[r], acc[1][m][4 * q + r] * scale[r]);
+            }
+    };
+    const int out_row = t0 + 4 * half, out_col = tile0 * 32 + (GATED ? row : 2 * row);
+    const bool whole = t0 + BM <= a.t && (tile0 + (GATED ? 1 : 2)) * 32 <= a.n && (GATED || !a.accumulate);
+    const size_t at = (size_t)out_row * a.ldo + out_col;
+    const bool even = GATED || (a.ldo & 1) == 0;
+    if (whole && even && a.out_type == MOE_BF16 && reinterpret_cast<uintptr_t>(a.out) % (GATED ? 2 : 4) == 0) {
+        uint16_t *p = static_cast<uint16_t *>(a.out) + at;
+        finish([&](int r, float u, float v) {
+            if constexpr (GATED) {
+                p[(size_t)r * a.ldo] = to_bf16(silu_mul(u, v));
+            } else {
+                const bf16x2 o = {(__bf16)u, (__bf16)v};
+                *reinterpret_cast<bf16x2 *>(p + (size_t)r * a.ldo) = o;
+            }
+        });
+    } else if (!F8 && whole && even && a.out_type == MOE_F32 && reinterpret_cast<uintptr_t>(a.out) % (GATED ? 4 : 8) == 0) {
+        float *p = static_cast<float *>(a.out) + at;
+        finish([&](int r, float u, float v) {
+            if constexpr (GATED) p[(size_t)r * a.ldo] = silu_mul(u, v);
+            else *reinterpret_cast<f32x2 *>(p + (size_t)r * a.ldo) = (f32x2){u, v};
+        });
+    } else {
+        finish([&](int r, float u, float v) {
+            float o[2] = {u, v};
+            store_units<GATED, GATED ? 1 : 2, GATED ? 32 : 1>(a, out_row + r, out_col, o);
+        });
+    }
 }
 
 template <int XT, int G, bool GATED, bool F8>

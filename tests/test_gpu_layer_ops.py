@@ -251,6 +251,23 @@ def test_long_chunk(t, n, k, kind, group):
     ref.check_rounded(out[pick], y + b, e + ref.U32 * (y.abs() + b.abs()), BF16, "accumulate")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("width,first", [(25670, 0), (25672, 0), (25672, 1), (25671, 0), (25680, 2)])
+def test_long_chunk_output_places(width, first, kind, dtype):
+    """Outputs that start at any element, rows any distance apart, whole blocks of 128 rows and part of one."""
+    t, n, k = 300, 25670, 128
+    m = ref.Matrix(n, k, 64, 5)
+    x, s, d = rows(t, k, 9, kind)
+    y, err = m.product(d)
+    if kind != "bf16" and dtype == BF16:
+        err = err + ref.e4m3_product_error(m, d)
+    buf = torch.full((t, width), GUARD, dtype=dtype, device="cuda")
+    device_matrix(m).linear(x, s, out=buf[:, first:first + n])
+    ref.check_rounded(buf[:, first:first + n], y, err, dtype, (width, first, kind, dtype))
+    assert bool((buf[:, :first] == GUARD).all() and (buf[:, first + n:] == GUARD).all())
+
+
 @pytest.mark.parametrize("group", [64, 32])
 @pytest.mark.parametrize("kind", ["bf16", "row", "block"])
 @pytest.mark.parametrize("t,n,k", [(70, 25600, 128), (1000, 3300, 704), (4096, 896, 1088)])
