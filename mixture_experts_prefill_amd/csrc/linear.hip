@@ -311,6 +311,35 @@ __device__ __forceinline__ float row_scale(const LinearArgs &a, int row) {
     return a.x_scale_kind == MOE_SCALE_ROW ? static_cast<const float *>(a.x_scale)[min(row, a.t - 1)] : 1.0f;
 }
 
+// Another lane's value: DPP moves inside 16 lanes cost one instruction, where
+// a shuffle goes through LDS.  0xb1 / 0x4e: lane ^ 1 / lane ^ 2; 0x141 / 0x140:
+// mirrored inside 8 / 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+// The largest of N adjacent lanes' values, N = 16 or 32, none of them negative
+// (their bits order as integers).
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+    uint32_t u = __float_as_uint(v);
+    u = max(u, dpp<0xb1>(u));
+    u = max(u, dpp<0x4e>(u));
+    u = max(u, dpp<0x141>(u));
+    u = max(u, dpp<0x140>(u));
+    if (N == 32) {
+        const u32x2 both = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        u = max(both.x, both.y);
+    }
+    return __uint_as_float(u);
+}
+// Four lanes' words as a 4 x 4 matrix of bytes, transposed: byte i of lane b
+// (b = lane % 4) becomes byte b of lane i.
+__device__ __forceinline__ uint32_t transpose4(uint32_t v, int lane) {
+    v = __builtin_amdgcn_perm(dpp<0xb1>(v), v, lane & 1 ? 0x03070105u : 0x06020400u);
+    return __builtin_amdgcn_perm(dpp<0x4e>(v), v, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
 // RH finished outputs of one row, columns col + (32 / RH) i (gated: then the
 // RH of the second matrix).  All lanes of a wave call it together; the 32 / RH
 // lanes of one row are adjacent, and together they hold 32 adjacent outputs,
@@ -325,9 +354,7 @@ __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int co
             float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < RH; ++i) m = fmaxf(m, q8::magnitude(v[i]));
-#pragma unroll
-            for (int off = SPAN / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-            const uint32_t byte = q8::block_byte(m);
+            const uint32_t byte = q8::block_byte(lanes_max<SPAN>(m));
 #pragma unroll
             for (int i = 0; i < RH; ++i) {
                 const int c = col + SPAN * i;
@@ -1009,17 +1036,16 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
             }
             return x;
         };
-        // The wave's own block's group sums.  e4m3: one more product, with ones.  Otherwise piece by piece
-        // beside the products: piece m with block m's.
+        // The wave's own block's group sums, kept to the step's end (stored at once, every product would wait
+        // for them).  e4m3: one more product, with ones.  Otherwise piece by piece beside the products: piece m
+        // with block m's.
         float sum[NG];
         if constexpr (F8) {
             const Rows own = rows_of(wave);
             constexpr int o = 0x38383838;  // 1.0
             const i32x8 one = {o, o, o, o, o, o, o, o};
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g,
-                          mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0]);
+            for (int g = 0; g < NG; ++g) sum[g] = mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0];
         } else {
 #pragma unroll
             for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
@@ -1072,12 +1098,13 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[1][MT - 1][r] = __builtin_fmaf(s[1][NG - 1], dp[r], acc[1][MT - 1][r]);
-        if constexpr (!F8) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NG; ++g) {
+            if constexpr (!F8) {  // the lane halves' parts
                 const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[g]), __float_as_uint(sum[g]), false, false);
-                store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, __uint_as_float(both.x) + __uint_as_float(both.y));
+                sum[g] = __uint_as_float(both.x) + __uint_as_float(both.y);
             }
+            store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, sum[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
         expand(kb + 1);  // (past the last step: never used)
@@ -1092,44 +1119,75 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     barrier_no_fence();
     fold((nkb - 1) / CHUNK);
 
-    // Outputs: without a test each, from one address a lane, where the block is
-    // whole and its pairs aligned (4096 x 4096 x 4096, e4m3 rows: 122 -> 112 us).
+    // Outputs, four rows of a lane at a time: without a test each, from one
+    // address a lane, where the block is whole and its words are aligned (4096 x
+    // 4096 x 4096, e4m3 rows: 122 -> 112 us; gated with e4m3 outputs, 8192 x 4096:
+    // 470 -> 400).
     auto finish = [&](auto put) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                f32x4 scale = {1.0f, 1.0f, 1.0f, 1.0f};
+                f32x4 scale = {1.0f, 1.0f, 1.0f, 1.0f}, u, v;
                 if (XT == MOE_E4M3) scale = *reinterpret_cast<const f32x4 *>(row_scales + 32 * m + 8 * q + 4 * half);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    put(32 * m + 8 * q + r, acc[0][m][4 * q + r] * scale[r], acc[1][m][4 * q + r] * scale[r]);
+                for (int r = 0; r < 4; ++r) {
+                    u[r] = acc[0][m][4 * q + r] * scale[r];
+                    v[r] = acc[1][m][4 * q + r] * scale[r];
+                }
+                put(32 * m + 8 * q, u, v);
             }
     };
     const int out_row = t0 + 4 * half, out_col = tile0 * 32 + (GATED ? row : 2 * row);
     const bool whole = t0 + BM <= a.t && (tile0 + (GATED ? 1 : 2)) * 32 <= a.n && (GATED || !a.accumulate);
+    auto aligned = [&](int elements, int size) {  // words of so many outputs
+        return a.ldo % elements == 0 && reinterpret_cast<uintptr_t>(a.out) % (elements * size) == 0;
+    };
     const size_t at = (size_t)out_row * a.ldo + out_col;
-    const bool even = GATED || (a.ldo & 1) == 0;
-    if (whole && even && a.out_type == MOE_BF16 && reinterpret_cast<uintptr_t>(a.out) % (GATED ? 2 : 4) == 0) {
+    if (whole && a.out_type == MOE_BF16 && aligned(GATED ? 1 : 2, 2)) {
         uint16_t *p = static_cast<uint16_t *>(a.out) + at;
-        finish([&](int r, float u, float v) {
-            if constexpr (GATED) {
-                p[(size_t)r * a.ldo] = to_bf16(silu_mul(u, v));
-            } else {
-                const bf16x2 o = {(__bf16)u, (__bf16)v};
-                *reinterpret_cast<bf16x2 *>(p + (size_t)r * a.ldo) = o;
+        finish([&](int r0, f32x4 u, f32x4 v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (GATED) p[(size_t)(r0 + r) * a.ldo] = to_bf16(silu_mul(u[r], v[r]));
+                else *reinterpret_cast<bf16x2 *>(p + (size_t)(r0 + r) * a.ldo) = (bf16x2){(__bf16)u[r], (__bf16)v[r]};
             }
         });
-    } else if (!F8 && whole && even && a.out_type == MOE_F32 && reinterpret_cast<uintptr_t>(a.out) % (GATED ? 4 : 8) == 0) {
+    } else if (!F8 && whole && a.out_type == MOE_F32 && aligned(GATED ? 1 : 2, 4)) {
         float *p = static_cast<float *>(a.out) + at;
-        finish([&](int r, float u, float v) {
-            if constexpr (GATED) p[(size_t)r * a.ldo] = silu_mul(u, v);
-            else *reinterpret_cast<f32x2 *>(p + (size_t)r * a.ldo) = (f32x2){u, v};
+        finish([&](int r0, f32x4 u, f32x4 v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (GATED) p[(size_t)(r0 + r) * a.ldo] = silu_mul(u[r], v[r]);
+                else *reinterpret_cast<f32x2 *>(p + (size_t)(r0 + r) * a.ldo) = (f32x2){u[r], v[r]};
+            }
+        });
+    } else if (GATED && whole && a.out_type == MOE_E4M3 && aligned(4, 1)) {
+        // codes of four rows, exchanged among four lanes: a lane stores four columns of row lane % 4
+        uint8_t *p = static_cast<uint8_t *>(a.out) + (size_t)(out_row + (lane & 3)) * a.ldo + tile0 * 32 + (row & ~3);
+        uint8_t *ps = a.out_scale + (size_t)(out_row + (lane & 3)) * (a.n / 32) + tile0;
+        finish([&](int r0, f32x4 u, f32x4 v) {
+            uint32_t bytes = 0, bad = 0;
+            float y[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float o = silu_mul(u[r], v[r]);
+                const uint32_t byte = q8::block_byte(lanes_max<32>(q8::magnitude(o)));
+                bytes |= byte << (8 * r);
+                bad |= q8::finite(o) ? 0u : q8::kNaN << (8 * r);
+                y[r] = o * q8::block_inverse(byte);
+            }
+            const uint32_t codes = __builtin_amdgcn_perm(q8::codes2(y[2], y[3]), q8::codes2(y[0], y[1]), 0x05040100u) | bad;
+            *reinterpret_cast<uint32_t *>(p + (size_t)r0 * a.ldo) = transpose4(codes, lane);
+            if (row < 4) ps[(size_t)r0 * (a.n / 32)] = (uint8_t)(bytes >> (8 * (lane & 3)));
         });
     } else {
-        finish([&](int r, float u, float v) {
-            float o[2] = {u, v};
-            store_units<GATED, GATED ? 1 : 2, GATED ? 32 : 1>(a, out_row + r, out_col, o);
+        finish([&](int r0, f32x4 u, f32x4 v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float o[2] = {u[r], v[r]};
+                store_units<GATED, GATED ? 1 : 2, GATED ? 32 : 1>(a, out_row + r0 + r, out_col, o);
+            }
         });
     }
 }

@@ -317,6 +317,34 @@ def test_long_chunk_bad_rows_and_bits():
             assert not bool(torch.isfinite(got[[77, 4095]]).any())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+@pytest.mark.parametrize("t", [3, 40, 300])
+def test_gated_8_bit_places_and_bad_rows(t, kind):
+    """8-bit outputs that start at any byte have the bits of aligned ones; a bad
+    row is NaN codes with the smallest scale, and stays alone."""
+    n, k = (12864 if t == 300 else 96), 128
+    g, u = device_matrix(ref.Matrix(n, k, 64, 1)), device_matrix(ref.Matrix(n, k, 64, 2))
+    x, s, _ = rows(t, k, 21, kind)
+    want, scale = g.gated(u, x, s, out_dtype=E4M3)
+    for width, first in ((n, 0), (n + 4, 4), (n + 4, 1), (n + 3, 0)):
+        buf = torch.full((t, width), 0x55, dtype=torch.uint8, device="cuda").view(E4M3)
+        got, gscale = g.gated(u, x, s, out=buf[:, first:first + n])
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8)) and torch.equal(gscale, scale)
+        rest = torch.cat([buf.view(torch.uint8)[:, :first], buf.view(torch.uint8)[:, first + n:]], 1)
+        assert bool((rest == 0x55).all())
+    bad = x.clone()
+    for r in (1, t - 1):
+        if kind == "bf16":
+            bad[r] = float("nan")
+        else:
+            bad.view(torch.uint8)[r] = 0x7F
+    got, gscale = g.gated(u, bad, s, out_dtype=E4M3)
+    keep = torch.ones(t, dtype=torch.bool, device="cuda")
+    keep[[1, t - 1]] = False
+    assert torch.equal(got.view(torch.uint8)[keep], want.view(torch.uint8)[keep]) and torch.equal(gscale[keep], scale[keep])
+    assert bool(((got.view(torch.uint8)[~keep] & 0x7F) == 0x7F).all()) and bool((gscale[~keep] == 0).all())
+
+
 def test_same_call_same_bits():
     for t in (1, 20, 200):
         m = ref.Matrix(300, 1024, 64)
