@@ -172,11 +172,14 @@ struct Frag {
 };
 
 // Rows of a step in LDS, written by DMA: 64 columns of each row, its 16-byte
-// parts exchanged so that one part of 8 neighbouring rows falls into different
-// banks.  part_at: where part p of row r is, relative to the row.
+// parts exchanged so that one part of the 16 rows that a read serves together
+// falls into different banks; these are not 16 neighbours, but rows 0-3, 12-15,
+// 20-23, 24-27 and the rest, as the bank conflict counter showed (a quarter of
+// the long chunks' time had conflicts with an order for neighbours, none of the
+// reads has now).  part_at: where part p of row r is, relative to the row.
 template <int XT>
 __device__ __forceinline__ int part_at(int p, int r) {
-    return (XT == MOE_BF16 ? p ^ (r & 7) : p ^ ((r >> 1) & 3)) * 16;
+    return (XT == MOE_BF16 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3)) * 16;
 }
 template <int XT>
 constexpr int kRowBytes = XT == MOE_BF16 ? 128 : 64;
@@ -928,11 +931,14 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[f][m] = (f32x16){};
+    // Sums and biases of a chunk: 16 groups a row or output, 32 bytes, whose halves change places in every
+    // other eight rows (32 rows then write one group's entries into twice as many banks).
     uint8_t *const sums = smem + 2 * XBUF, *const biases = sums + 2 * SUMS + wave * (2 * BIAS);
+    const int entry = row * 32 + (row & 8) * 2;
     // Group sum v of row `row` of block `wave`: its three terms into slot `slot` of the chunk's buffer.
     // (both lane halves write the same).
     auto store_sum = [&](int chunk, int slot, float v) {
-        uint8_t *p = sums + (chunk & 1) * SUMS + (32 * wave + row) * 32 + slot * 2;
+        uint8_t *p = sums + (chunk & 1) * SUMS + wave * 1024 + (entry ^ slot * 2);
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
             const uint32_t h = __float_as_uint(v) & 0xffff0000u;
@@ -941,14 +947,14 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
     };
     auto store_bias = [&](int chunk, int f, int slot, uint16_t b) {
-        *reinterpret_cast<uint16_t *>(biases + (chunk & 1) * BIAS + (f * 32 + row) * 32 + slot * 2) = b;
+        *reinterpret_cast<uint16_t *>(biases + (chunk & 1) * BIAS + f * 1024 + (entry ^ slot * 2)) = b;
     };
     // The biases' part of a chunk of 16 groups.
     auto fold = [&](int chunk) {
         bf16x8 bh[2], bl[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const u32x4 e = *reinterpret_cast<const u32x4 *>(biases + (chunk & 1) * BIAS + (f * 32 + row) * 32 + half * 16);
+            const u32x4 e = *reinterpret_cast<const u32x4 *>(biases + (chunk & 1) * BIAS + f * 1024 + (entry ^ half * 16));
             u32x4 h, l;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -964,7 +970,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint8_t *p = sums + (chunk & 1) * SUMS + (32 * m + row) * 32 + half * 16;
+            const uint8_t *p = sums + (chunk & 1) * SUMS + m * 1024 + (entry ^ half * 16);
             const bf16x8 x0 = *reinterpret_cast<const bf16x8 *>(p);
             const bf16x8 x1 = *reinterpret_cast<const bf16x8 *>(p + BM * 32);
             const bf16x8 x2 = *reinterpret_cast<const bf16x8 *>(p + 2 * BM * 32);
