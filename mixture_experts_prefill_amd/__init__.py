@@ -73,7 +73,7 @@ EXPORTS = ["moe_last_error", "moe_layout_make", "moe_workspace_bytes", "moe_rout
            "moe_linear", "moe_linear_gated", "moe_residual_norm"]
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 PHASES = ["router", "topk", "csr", "shared_gateup", "shared_down", "schedule", "gateup", "down", "combine", "norm",
-          "experts"]
+          "experts", "linear"]  # MOE_PHASE_* in order; moe_profile_end fills one entry each
 
 
 def lib():

@@ -4,6 +4,7 @@ checks (the pointers are never dereferenced).
 """
 import ctypes
 import os
+import re
 
 import numpy as np
 import pytest
@@ -193,3 +194,15 @@ def test_python_refuses_before_the_library(lib):
     for bad in (torch.zeros(3), torch.zeros(2, 2, dtype=torch.float16), torch.zeros(2, 4, dtype=torch.uint8)[:, ::2]):
         with pytest.raises(ValueError):
             mep._scale_args(bad, 2, 64, 0, "scale")
+
+
+def test_profile_phases_are_the_librarys(lib):
+    """moe_profile_end writes as many entries as the binding has names (a shorter
+    list would make it write past the binding's arrays), in the header's order."""
+    total, launches = np.full(64, -1.0), np.full(64, -1, np.int64)
+    assert lib.moe_profile_end(total.ctypes.data, launches.ctypes.data) == 0
+    assert int((total == 0).sum()) == int((launches == 0).sum()) == len(mep.PHASES)
+    with open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "include", "moe_debug.h")) as f:
+        header = dict(re.findall(r"MOE_PHASE_?(\w+) = (\d+)", f.read()))
+    assert int(header.pop("S")) == len(mep.PHASES) == len(header)
+    assert mep.PHASES[int(header["LINEAR"])] == "linear"
