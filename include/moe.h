@@ -578,7 +578,8 @@ moe_status moe_linear_gated(const void *x, int32_t x_type, int64_t ldx, const vo
  *   y = s * gamma / sqrt(mean(s^2) + eps)                -> out (bf16), codes
  *
  * The norm is that of the stored (rounded) stream, so it can be recomputed
- * from it.  8-bit rows: per row scale = max(max|y| / 448, 2^-126); per block
+ * from it; its sum of squares is fp32, and has to stay inside fp32's range.
+ * 8-bit rows: per row scale = max(max|y| / 448, 2^-126); per block
  * of 32 columns the smallest power of two 2^E, -127 <= E <= 127, with
  * max|y| <= 448 * 2^E (E = -127 for a block of zeros), stored as E + 127;
  * codes are y / scale rounded to nearest even, at most +-448.  A y that is
