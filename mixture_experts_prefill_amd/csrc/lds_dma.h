@@ -56,13 +56,6 @@ __device__ __forceinline__ void dma4(uint32_t lds_addr, uint32_t voff, i32x4 rsr
                  : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory", "m0");
 }
-// One byte per lane, zero-extended to a word: lane i's word lands at m0 + 4i.
-__device__ __forceinline__ void dma1(uint32_t lds_addr, uint32_t voff, i32x4 rsrc, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
-}
 
 // The same loads with the non-temporal hint, for weights that one workgroup
 // streams once: they then do not displace the activations, router weights

@@ -93,6 +93,14 @@ __device__ __forceinline__ uint32_t load1(const uint8_t *p) {
     return *reinterpret_cast<const GLOBAL uint8_t *>(reinterpret_cast<uintptr_t>(p));
 }
 
+// One byte per lane, zero-extended to a word: lane i's word lands at m0 + 4i.
+__device__ __forceinline__ void dma1(uint32_t lds_addr, uint32_t voff, i32x4 rsrc, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+}
+
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
