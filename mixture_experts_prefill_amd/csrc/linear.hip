@@ -27,9 +27,10 @@
 // 0..7 are the subnormals, 8..15 the first binade, one straight line), so
 // v_cvt_scalef32_pk_bf16_fp8 with 2^9 gives two exact bf16 codes.  8-bit rows
 // become bf16 by the same instruction, block scale included, exactly: the bf16
-// MFMA adds its products up to about 1e-7 of their largest (measured), where
-// the e4m3 MFMA, of twice the rate, keeps about 16 bits (2.5e-5); that one
-// serves long chunks whose outputs are rounded to 8 bits or fewer anyway.
+// MFMA adds its products up to about 1e-7 of their largest (measured), as fp32
+// sums do.  The e4m3 MFMA, of twice the rate, keeps about 16 bits (2.5e-5) of
+// it: one strong channel with a weight near 0 would leave the others' sum wrong
+// by its own size, whatever type the output is rounded to, so it is not used.
 //
 // Times here are medians of a kernel on one otherwise idle MI355X, inputs cold
 // in the caches of the call before; where two stand, both were timed in turn.
@@ -55,7 +56,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 #define GLOBAL __attribute__((address_space(1)))
 
 __device__ __forceinline__ u32x4 load16(const uint8_t *p) {
@@ -146,11 +146,7 @@ __device__ __forceinline__ float add_pair(uint32_t u, float v) {
 __device__ __forceinline__ f32x16 mfma_bf16(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-// e4m3 operands, each lane's first and second 16 values scaled by 2^(scale - 127).
-__device__ __forceinline__ f32x16 mfma_e4m3(i32x8 a, i32x8 b, f32x16 c, int a_scale, int b_scale) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, a_scale, 0, b_scale);
-}
-constexpr int kScaleOne = 127, kScaleCode = 127 + 9;
+constexpr uint32_t kScaleOne = 127;  // byte of a block scale of 1
 
 // SiLU(g) * u; exp overflows to infinity for g below about -88, where the quotient is -0.
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
@@ -257,29 +253,6 @@ __device__ __forceinline__ f32x16 group_sum(const Frag &x, int gi) {
     for (int i = 0; i < 4; ++i)
         if (G == 64 || (i & 1) == gi) d = mfma_bf16(x.v[i], one, d);
     return d;
-}
-
-// The operands of the e4m3 MFMA (32x32x64).  The lane halves take alternate 16
-// bytes of a step's 64 columns: a lane's first 16 bytes belong to the first 32
-// columns, the others to the second, and the scale operand of lane half h is
-// that of the h-th 32 columns.  Codes: a byte 0..15 is q * 2^-9, the scale
-// brings 2^9; words are exchanged between the lane halves first.
-__device__ __forceinline__ i32x8 w_frag8(u32x4 w) {
-    const u32x2 p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
-    const u32x2 q = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-    const u32x2 a = code_bytes(p.x), b = code_bytes(q.x), c = code_bytes(p.y), d = code_bytes(q.y);
-    return (i32x8){(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
-}
-// at: LDS address of the lane's first 16 bytes (part `half`).
-__device__ __forceinline__ i32x8 x_frag8(uint32_t at) {
-    const u32x4 a = lds_read<u32x4>(at), b = lds_read<u32x4>(at ^ 32);
-    return (i32x8){(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-// Group gi alone (groups of 32): the other one's 16 bytes 0.
-template <int G>
-__device__ __forceinline__ i32x8 group_of(i32x8 v, int gi) {
-    if (G == 64) return v;
-    return gi ? (i32x8){0, 0, 0, 0, v[4], v[5], v[6], v[7]} : (i32x8){v[0], v[1], v[2], v[3], 0, 0, 0, 0};
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -852,9 +825,8 @@ hipError_t launch_units(const LinearArgs &a, hipStream_t s) {
 // block by output block, so that the workgroups of an XCD that run together
 // share both rows and codes in its L2.
 constexpr int kBand = 8;
-template <int XT, int G, bool GATED, bool F8>
+template <int XT, int G, bool GATED>
 __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
-    static_assert(!F8 || XT == MOE_E4M3, "e4m3 products are of e4m3 rows");
     constexpr int MT = 4;  // blocks of 32 rows; each of the four waves sums one
     constexpr int NM = GATED ? 2 : 1;
     constexpr int BM = 32 * MT, NG = 64 / G, CHUNK = 16 / NG;  // steps per fold of 16 groups
@@ -933,7 +905,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
                 sv[f][g] = buffer_load4(sb[f % NM], so + (GATED ? 0 : f * 4) + g * 128, kb * (128 * NG));
         }
     };
-    const uint32_t x_at = lds_base + row * ROW + (F8 ? part_at<XT>(half, row) : piece_at<XT, G>(row, half));
+    const uint32_t x_at = lds_base + row * ROW + piece_at<XT, G>(row, half);
     f32x16 acc[2][MT];
 #pragma unroll
     for (int f = 0; f < 2; ++f)
@@ -994,13 +966,12 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     };
 
     // Step kb's codes, loaded, as operands.
-    typename std::conditional<F8, i32x8, Frag>::type wf[2];
+    Frag wf[2];
     float s[2][NG];
     auto expand = [&](int kb) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            if constexpr (F8) wf[f] = w_frag8(w[f]);
-            else wf[f] = w_frag<G>(w[f]);
+            wf[f] = w_frag<G>(w[f]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 s[f][g] = in_f32(__builtin_bit_cast(half2_t, sv[f][g]).x);
@@ -1030,81 +1001,56 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         const uint32_t *xsb = reinterpret_cast<const uint32_t *>(smem + scales_at + (kb & 1) * SCALES) + row * 2;
         // Rows of block m as operands.  No branch in here: it would part the
         // schedule, and every product of the step would wait at its end.
-        struct Rows {
-            typename std::conditional<F8, i32x8, Frag>::type v;
-            int scale;
-        };
         auto rows_of = [&](int m) {
-            Rows x;
-            x.scale = kScaleOne;
-            if constexpr (F8) {
-                x.v = x_frag8(xb + m * 32 * ROW);
-                x.scale = (int)xsb[m * 64 + half];
-            } else {
-                float scale[2] = {1.0f, 1.0f};
-                if constexpr (XT == MOE_E4M3) {
-                    scale[0] = __uint_as_float(xsb[m * 64 + (G == 64 ? half : 0)] << 23);
-                    scale[1] = G == 64 ? scale[0] : __uint_as_float(xsb[m * 64 + 1] << 23);
-                }
-                x.v = x_frag<XT, G>(xb + m * 32 * ROW, scale);
+            float scale[2] = {1.0f, 1.0f};
+            if constexpr (XT == MOE_E4M3) {
+                scale[0] = __uint_as_float(xsb[m * 64 + (G == 64 ? half : 0)] << 23);
+                scale[1] = G == 64 ? scale[0] : __uint_as_float(xsb[m * 64 + 1] << 23);
             }
-            return x;
+            return x_frag<XT, G>(xb + m * 32 * ROW, scale);
         };
-        // The wave's own block's group sums, kept to the step's end (stored at once, every product would wait
-        // for them).  e4m3: one more product, with ones.  Otherwise piece by piece beside the products: piece m
-        // with block m's.
+        // The wave's own block's group sums, piece by piece beside the products, piece m with block m's, kept to
+        // the step's end (stored at once, every product would wait for them).
         float sum[NG];
-        if constexpr (F8) {
-            const Rows own = rows_of(wave);
-            constexpr int o = 0x38383838;  // 1.0
-            const i32x8 one = {o, o, o, o, o, o, o, o};
 #pragma unroll
-            for (int g = 0; g < NG; ++g) sum[g] = mfma_e4m3(one, group_of<G>(own.v, g), (f32x16){}, kScaleOne, own.scale)[0];
-        } else {
-#pragma unroll
-            for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
-        }
+        for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
         float own_scale[2] = {1.0f, 1.0f};
-        if constexpr (!F8 && XT == MOE_E4M3) {
+        if constexpr (XT == MOE_E4M3) {
             own_scale[0] = __uint_as_float(xsb[wave * 64 + (G == 64 ? half : 0)] << 23);
             own_scale[1] = G == 64 ? own_scale[0] : __uint_as_float(xsb[wave * 64 + 1] << 23);
         }
         // Products in order (block, group, tile); each one's multiply-adds run beside the next one's MFMAs.
-        // The next block's rows are read meanwhile; bf16 operands of groups of 32 group by group, each into the
-        // registers of the group just used (with registers of their own the compiler spills to memory).
-        constexpr bool BY_GROUP = !F8 && G == 32;
-        Rows xf = rows_of(0);
+        // The next block's rows are read meanwhile; those of groups of 32 group by group, each into the registers
+        // of the group just used (with registers of their own the compiler spills more to memory).
+        constexpr bool BY_GROUP = G == 32;
+        Frag xf = rows_of(0);
         f32x16 dp;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            Rows xn;
-            bf16x8 own;
-            if constexpr (!F8) own = x_piece<XT, G>(xb + wave * 32 * ROW, m, own_scale);
+            Frag xn;
+            const bf16x8 own = x_piece<XT, G>(xb + wave * 32 * ROW, m, own_scale);
 #pragma unroll
             for (int p = 0; p < 2 * NG; ++p) {
                 const int g = p / 2, f = p % 2;
-                f32x16 d;
-                if constexpr (F8) d = mfma_e4m3(xf.v, group_of<G>(wf[f], g), (f32x16){}, xf.scale, kScaleCode);
-                else d = group_product<G>(xf.v, wf[f], g);
+                const f32x16 d = group_product<G>(xf, wf[f], g);
                 if (!BY_GROUP && p == 0 && m + 1 < MT) xn = rows_of(m + 1);
                 if constexpr (BY_GROUP)
                     if (f == 1 && m + 1 < MT) {
                         float scale[2] = {1.0f, 1.0f};
                         if (XT == MOE_E4M3) scale[g] = __uint_as_float(xsb[(m + 1) * 64 + g] << 23);
-                        xf.v.v[g] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g, scale);
-                        xf.v.v[g + 2] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g + 2, scale);
+                        xf.v[g] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g, scale);
+                        xf.v[g + 2] = x_piece<XT, G>(xb + (m + 1) * 32 * ROW, g + 2, scale);
                     }
                 if (m || p) {
                     const int pm = p ? m : m - 1, pg = p ? (p - 1) / 2 : NG - 1, pf = (p + 1) % 2;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[pf][pm][r] = __builtin_fmaf(s[pf][pg], dp[r], acc[pf][pm][r]);
                 }
-                if constexpr (!F8)
-                    if (p == 1) {
-                        const u32x4 u = __builtin_bit_cast(u32x4, own);
+                if (p == 1) {
+                    const u32x4 u = __builtin_bit_cast(u32x4, own);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sum[NG == 1 ? 0 : m & 1] = add_pair(u[j], sum[NG == 1 ? 0 : m & 1]);
-                    }
+                    for (int j = 0; j < 4; ++j) sum[NG == 1 ? 0 : m & 1] = add_pair(u[j], sum[NG == 1 ? 0 : m & 1]);
+                }
                 __builtin_amdgcn_sched_barrier(0);
                 dp = d;
             }
@@ -1114,10 +1060,9 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
         for (int r = 0; r < 16; ++r) acc[1][MT - 1][r] = __builtin_fmaf(s[1][NG - 1], dp[r], acc[1][MT - 1][r]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            if constexpr (!F8) {  // the lane halves' parts
-                const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[g]), __float_as_uint(sum[g]), false, false);
-                sum[g] = __uint_as_float(both.x) + __uint_as_float(both.y);
-            }
+            // the lane halves' parts
+            const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[g]), __float_as_uint(sum[g]), false, false);
+            sum[g] = __uint_as_float(both.x) + __uint_as_float(both.y);
             store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, sum[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -1167,7 +1112,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
                 else *reinterpret_cast<bf16x2 *>(p + (size_t)(r0 + r) * a.ldo) = (bf16x2){(__bf16)u[r], (__bf16)v[r]};
             }
         });
-    } else if (!F8 && whole && a.out_type == MOE_F32 && aligned(GATED ? 1 : 2, 4)) {
+    } else if (whole && a.out_type == MOE_F32 && aligned(GATED ? 1 : 2, 4)) {
         float *p = static_cast<float *>(a.out) + at;
         finish([&](int r0, f32x4 u, f32x4 v) {
 #pragma unroll
@@ -1206,19 +1151,11 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
     }
 }
 
-template <int XT, int G, bool GATED, bool F8>
-hipError_t launch_many_as(const LinearArgs &a, hipStream_t s) {
-    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 127) / 128);
-    hipLaunchKernelGGL((k_linear_many<XT, G, GATED, F8>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
 template <int XT, int G, bool GATED>
 hipError_t launch_many(const LinearArgs &a, hipStream_t s) {
-    // The e4m3 MFMA adds its 64 products to about 16 bits: enough for outputs
-    // of 8 bits of mantissa or fewer, not for fp32 ones.
-    if constexpr (XT == MOE_E4M3)
-        if (a.out_type != MOE_F32) return launch_many_as<XT, G, GATED, true>(a, s);
-    return launch_many_as<XT, G, GATED, false>(a, s);
+    const int obs = (a.n + 31) / 32, tiles = GATED ? 4 : 8, total = (obs + tiles - 1) / tiles * ((a.t + 127) / 128);
+    hipLaunchKernelGGL((k_linear_many<XT, G, GATED>), dim3((total + 7) / 8 * 8), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 template <int XT, int G, bool GATED, int MT, int NT>
