@@ -6,11 +6,22 @@ layout and output allocation live here; the arithmetic is in libmoe.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
 
 from . import moe_linear, moe_linear_gated, moe_matrix_layout_make
+
+
+def _allocating_on(stream, device: torch.device):
+    """A context whose allocations belong to the stream that the kernel runs on
+    (memory of the current stream's pool may still be written by what is queued there)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 class MoeMatrix:
@@ -50,11 +61,13 @@ class MoeMatrix:
 
     def linear(self, x: torch.Tensor, x_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                out_dtype: torch.dtype = torch.bfloat16, accumulate: int = 0, stream=None) -> torch.Tensor:
-        """x times this matrix (moe_linear), into `out` or a new tensor."""
+        """x times this matrix (moe_linear), into `out` or a new tensor, which is
+        `stream`'s like any tensor allocated on it."""
         if out is None:
             if accumulate:
                 raise ValueError("accumulate adds into a given out")
-            out = torch.empty((x.shape[0], self.n), dtype=out_dtype, device=x.device)
+            with _allocating_on(stream, x.device):
+                out = torch.empty((x.shape[0], self.n), dtype=out_dtype, device=x.device)
         moe_linear(x, self.layout, self.record, out, x_scale, accumulate, stream)
         return out
 
@@ -62,12 +75,14 @@ class MoeMatrix:
               out: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None,
               out_dtype: torch.dtype = torch.bfloat16, stream=None):
         """silu(x times this matrix) * (x times `up`) (moe_linear_gated); with
-        8-bit output returns (codes, scale)."""
+        8-bit output returns (codes, scale).  New tensors are `stream`'s."""
         if (up.n, up.k, up.group) != (self.n, self.k, self.group):
             raise ValueError("gate and up must have the same shape and group")
-        if out is None:
-            out = torch.empty((x.shape[0], self.n), dtype=out_dtype, device=x.device)
-        if out.dtype == torch.float8_e4m3fn and out_scale is None:
-            out_scale = torch.empty((x.shape[0], self.n // 32), dtype=torch.uint8, device=x.device)
+        if out is None or (out.dtype == torch.float8_e4m3fn and out_scale is None):
+            with _allocating_on(stream, x.device):
+                if out is None:
+                    out = torch.empty((x.shape[0], self.n), dtype=out_dtype, device=x.device)
+                if out.dtype == torch.float8_e4m3fn and out_scale is None:
+                    out_scale = torch.empty((x.shape[0], self.n // 32), dtype=torch.uint8, device=x.device)
         moe_linear_gated(x, self.layout, self.record, up.record, out, x_scale, out_scale, stream)
         return out if out_scale is None else (out, out_scale)
