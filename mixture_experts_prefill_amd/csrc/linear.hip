@@ -101,6 +101,10 @@ __device__ __forceinline__ void dma1(uint32_t lds_addr, uint32_t voff, i32x4 rsr
                  : "memory", "m0");
 }
 
+// Everything that this wave has asked for: rows on their way into LDS, and its
+// reads of the buffer that the next rows go to (vmcnt(0), lgkmcnt(0)).
+__device__ __forceinline__ void wait_rows_and_reads() { __builtin_amdgcn_s_waitcnt(7 << 4); }
+
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
@@ -467,11 +471,11 @@ __global__ void __launch_bounds__(64 * kMaxWaves) k_linear_split(LinearArgs a) {
         int kb = k0;
         load(b0, kb);
         while (true) {
-            wait_vm<0>();
+            wait_rows_and_reads();
             if (kb + 1 < k1) load(b1, kb + 1);
             compute(b0, kb);
             if (++kb >= k1) break;
-            wait_vm<0>();
+            wait_rows_and_reads();
             if (kb + 1 < k1) load(b0, kb + 1);
             compute(b1, kb);
             if (++kb >= k1) break;
@@ -982,15 +986,17 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
 
     // Rows are loaded at the start of the step before their own; codes at the
     // end of the step but one before, expanded at the end of the step before.
-    constexpr int CODE_LOADS = 2 * (1 + NG);
+    // Rows are waited for before the next codes go out: later the wait would have
+    // to count those loads, which the compiler is free to merge.  It costs
+    // nothing, as the compiler, which does not know of the rows' loads, waits for
+    // everything in front of expand by itself.
     load_rows(0);
     load_codes(0);
+    wait_vm<0>();
     expand(0);
     load_codes(min(1, nkb - 1));
     for (int kb = 0; kb < nkb; ++kb) {
-        // this step's rows are in (only the next codes, loaded after them, may be on their way); every wave is
-        // done with the buffer that the next step's rows go to
-        wait_vm<CODE_LOADS>();
+        // every wave's rows of this step are in, and it is done with the buffer that the next step's go to
         barrier_no_fence();
         if (kb + 1 < nkb) load_rows(kb + 1);
         if (kb > 0 && kb % CHUNK == 0) fold(kb / CHUNK - 1);
@@ -1066,6 +1072,7 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
             store_sum(kb / CHUNK, (kb % CHUNK) * NG + g, sum[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        wait_vm<0>();
         expand(kb + 1);  // (past the last step: never used)
         load_codes(min(kb + 2, nkb - 1));
     }
