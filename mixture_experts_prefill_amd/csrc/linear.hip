@@ -152,8 +152,13 @@ __device__ __forceinline__ f32x16 mfma_bf16(bf16x8 a, bf16x8 b, f32x16 c) {
 }
 constexpr uint32_t kScaleOne = 127;  // byte of a block scale of 1
 
-// SiLU(g) * u; exp overflows to infinity for g below about -88, where the quotient is -0.
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// SiLU(g) * u, off by at most six half steps of fp32.  exp(-|g|) neither
+// overflows, which would lose the g below -88 whose SiLU a large u makes count,
+// nor comes from the fast exp, whose error grows with |g| (40 half steps at -60).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    const float e = expf(-__builtin_fabsf(g));
+    return (g < 0.0f ? g * e : g) / (1.0f + e) * u;
+}
 
 // Column of piece i of a lane's rows in a 64-column step, 8 columns each, the
 // lane's part of the step's MFMA i: with groups of 64 the pieces are a lane

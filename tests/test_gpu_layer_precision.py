@@ -37,3 +37,27 @@ def test_a_strong_channel_leaves_the_others_sums(t, n, k, kind, group):
     for dtype in (F32, BF16):
         got = dm.linear(dc, ds, out_dtype=dtype)[:, cols.cuda()]
         ref.check_rounded(got, y, err, dtype, (t, n, k, kind, group, dtype))
+
+
+@pytest.mark.parametrize("t,n", [(3, 64), (16, 64), (40, 64), (150, 25600)])
+def test_silu_keeps_fp32(t, n):
+    """Exact gates -100 .. 100 (one product each) and exact up values: what is off is the activation's alone.
+    exp within one step (two half steps), then a product, a sum, a quotient and the product with up, half a step
+    each: six half steps; where exp leaves fp32's normal range, half a step of 2^-149 times the gate."""
+    k = 64
+    a = torch.linspace(-6.66, 6.66, t).to(BF16)
+    x = torch.zeros(t, k, dtype=BF16)
+    x[:, 0], x[:, 1] = a, 2.0 ** 20
+    mats = []
+    for first, second in ((torch.arange(n) % 16, 0), (0, torch.arange(n) % 13 + 1)):
+        m = ref.Matrix(n, k, 64)
+        m.q[:], m.s[:], m.b[:] = 0, 1.0, 0.0
+        m.q[:, 0], m.q[:, 1] = first, second
+        mats.append(m)
+    g, u = (x.double() @ m.values().t() for m in mats)
+    y = g / (1 + torch.exp(-g)) * u
+    tol = 6 * ref.U32 * y.abs() + (g.abs() + 1) * u.abs() * 2.0 ** -149 + 2.0 ** -149
+    out = device_matrix(mats[0]).gated(device_matrix(mats[1]), x.cuda(), out_dtype=F32).double().cpu()
+    bad = ~((out - y).abs() <= tol)
+    worst = (out - y).abs() / (ref.U32 * y.abs()).clamp_min(2.0 ** -149)
+    assert not bad.any(), (t, n, int(bad.sum()), float(worst.max()), float(g.flatten()[worst.argmax()]))
