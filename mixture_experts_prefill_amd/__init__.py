@@ -469,6 +469,8 @@ def _scale_args(scale: Optional[torch.Tensor], t: int, width: int, dev: int, wha
         kind, n = SCALE_ROW, t
     elif scale.dtype in _BLOCK_SCALE_TYPES:
         kind, n = SCALE_BLOCK, t * (width // 32)
+        if t > 1 and scale.dim() > 1 and scale.shape[-1] != width // 32:
+            raise ValueError(f"{what} must be [{t}, {width // 32}], one per 32 columns of a row, not {list(scale.shape)}")
     else:
         raise ValueError(f"{what} must be float32 (one a row) or uint8 / float8_e8m0fnu (one per 32 columns)")
     return _flat(scale, n, dev, what), kind
