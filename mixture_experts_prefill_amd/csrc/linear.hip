@@ -311,10 +311,11 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-// The largest of N adjacent lanes' values, N = 16 or 32, none of them negative
-// (their bits order as integers).
+// The largest of N adjacent lanes' values, none of them negative (their bits
+// order as integers).
 template <int N>
 __device__ __forceinline__ float lanes_max(float v) {
+    static_assert(N == 16 || N == 32, "16 or 32 lanes");
     uint32_t u = __float_as_uint(v);
     u = max(u, dpp<0xb1>(u));
     u = max(u, dpp<0x4e>(u));
@@ -333,16 +334,19 @@ __device__ __forceinline__ uint32_t transpose4(uint32_t v, int lane) {
     return __builtin_amdgcn_perm(dpp<0x4e>(v), v, lane & 2 ? 0x03020706u : 0x05040100u);
 }
 
-// RH finished outputs of one row, columns col + (32 / RH) i (gated: then the
-// RH of the second matrix).  All lanes of a wave call it together; the 32 / RH
-// lanes of one row are adjacent, and together they hold 32 adjacent outputs,
-// the block of an 8-bit output's scale.
-template <bool GATED, int RH, int SPAN = 32 / RH>
+// RH finished outputs of one row, columns col + SPAN i (gated: then the RH of
+// the second matrix).  All lanes of a wave call it together.  8-bit outputs need
+// a scale's whole block, 32 adjacent outputs of a row, in SPAN adjacent lanes of
+// RH outputs each; other instantiations have no such path, and the host sends
+// them no such call (launch_units_rows: a wave owns a pair of units then).
+template <bool GATED, int RH, int SPAN>
 __device__ __forceinline__ void store_units(const LinearArgs &a, int row, int col, float *v) {
     const bool live = row < a.t;
-    if (GATED) {
+    if constexpr (GATED) {
 #pragma unroll
         for (int i = 0; i < RH; ++i) v[i] = silu_mul(v[i], v[RH + i]);
+    }
+    if constexpr (GATED && RH * SPAN == 32) {
         if (a.out_type == MOE_E4M3) {
             float m = 0.0f;
 #pragma unroll
