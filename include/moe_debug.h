@@ -32,6 +32,9 @@ int moe_ring_plan_debug(const uint32_t *offsets, const uint64_t *resident, int32
  * and launch counts per phase into ms[MOE_PHASES] and launches[MOE_PHASES]
  * (either may be NULL), and stops recording.  Returns the number of timed
  * launches, or -1 on a HIP error.  Not thread safe; meant for benchmarks.
+ * MOE_PHASES grows when the library times a new phase, and moe_profile_end
+ * writes that many entries: a program is built with the header of the library
+ * that it loads, or passes arrays of 32 (a mask has no more phases).
  */
 enum {
     MOE_PHASE_ROUTER = 0,      /* router logits */

@@ -188,8 +188,8 @@ struct Frag {
 // parts exchanged so that one part of the 16 rows that a read serves together
 // falls into different banks; these are not 16 neighbours, but rows 0-3, 12-15,
 // 20-23, 24-27 and the rest, as the bank conflict counter showed (a quarter of
-// the long chunks' time had conflicts with an order for neighbours, none of the
-// reads has now).  part_at: where part p of row r is, relative to the row.
+// the long chunks' time had conflicts with an order for neighbours; 6% has now
+// with bf16 rows, 17% with e4m3 ones, read 8 bytes at a time).  part_at: where part p of row r is, relative to the row.
 template <int XT>
 __device__ __forceinline__ int part_at(int p, int r) {
     return (XT == MOE_BF16 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3)) * 16;
@@ -1096,8 +1096,8 @@ __global__ void __launch_bounds__(256, 2) k_linear_many(LinearArgs a) {
 
     // Outputs, four rows of a lane at a time: without a test each, from one
     // address a lane, where the block is whole and its words are aligned (4096 x
-    // 4096 x 4096, e4m3 rows: 122 -> 112 us; gated with e4m3 outputs, 8192 x 4096:
-    // 470 -> 400).
+    // 4096 x 4096: 144 -> 139 us with bf16 rows, 162 -> 156 with e4m3; gated with
+    // e4m3 rows and outputs, 8192 x 4096: 640 -> 611).
     auto finish = [&](auto put) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -1199,10 +1199,14 @@ hipError_t launch_split(const LinearArgs &a, hipStream_t s) {
 }
 
 // Which kernel.  Up to 16 rows the codes' bytes bound the call.  The 128-row
-// tiles of k_linear_many pay from about 200 workgroups on (2048 x 4096 x 4096,
-// 256 of them: 99 us, against 125 split; 1024 x 4096 x 4096, 128: 95 against
-// 58), and if half of their rows are live (80 x 100003 x 2048: 82 us against
-// 91; 64 rows: 78 against 63).
+// tiles of k_linear_many pay from about 200 workgroups on (bf16 rows, 2048 x
+// 4096 x 4096, 256 of them: 83 us, against 112 split; 1024 x 4096 x 4096, 128: 81
+// against 66), and if half of their rows are live (80 x 100003 x 2048: 76 us
+// against 91; 64 rows: 78 against 66).  e4m3 rows gain less: 94 us against 109 at
+// 2048 rows, 93 against 65 at 1024, 90 against 89 at 80, and 1600 rows (208
+// workgroups) lose, 97 against 93.  So do groups of 32, whose long chunks spill,
+// at 256 workgroups (2048 rows: 177 us against 132, e4m3 164 against 145); at 512
+// they gain (4096 rows: 207 against 257, e4m3 202 against 280).
 constexpr long kManyWorkgroups = 200;
 constexpr int kManyRows = 65;
 template <int XT, int G, bool GATED>
