@@ -189,7 +189,8 @@ struct Frag {
 // falls into different banks; these are not 16 neighbours, but rows 0-3, 12-15,
 // 20-23, 24-27 and the rest, as the bank conflict counter showed (a quarter of
 // the long chunks' time had conflicts with an order for neighbours; 6% has now
-// with bf16 rows, 17% with e4m3 ones, read 8 bytes at a time).  part_at: where part p of row r is, relative to the row.
+// with bf16 rows, 17% with e4m3 ones, read 8 bytes at a time).  part_at: where
+// part p of row r is, relative to the row.
 template <int XT>
 __device__ __forceinline__ int part_at(int p, int r) {
     return (XT == MOE_BF16 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3)) * 16;
