@@ -599,6 +599,170 @@ moe_status moe_residual_norm(const void *x, int32_t x_type, int64_t ldx, const v
                              uint16_t *out, int64_t ldo, uint8_t *codes, int64_t ldc, void *scale,
                              int32_t scale_kind, void *stream);
 
+/*
+ * Attention over a paged key-value cache: what a layer runs between its
+ * q/k/v projection and its output projection (prefill.rs page, fn pf_layer:
+ * pf_attention over the chunk's rows; decode.rs page, fn step_rows: the same
+ * for one row a sequence).  A step is
+ *
+ *   moe_kv_plan            lengths -> pages, positions and slots of the rows
+ *   per layer:
+ *     moe_kv_append        k, v rows (k and q rotated) -> cache, q
+ *     moe_attention_decode (at most one row a sequence) or
+ *     moe_attention_prefill (any number)
+ *
+ * One plan serves all layers: they share the page tables, and each has a
+ * cache of its own.  All calls only read lengths, tables and slots on the
+ * GPU, launch a number of kernels that depends on nothing in them, and may
+ * be captured into a graph.  Integers are int32.
+ *
+ * The cache: `pages` pages of `page` tokens for `heads` key heads of `head`
+ * values, bf16 or e4m3 codes with one power-of-two scale per token and head
+ * (value = code * 2^(scale - 127), MOE_SCALE_BLOCK's byte over the whole
+ * head).  A slot is a token's place, page * (page size) + token in the page.
+ * The bytes stand as the matrix core reads them, in cells of 16 bytes (C = 8
+ * bf16 or 16 e4m3 values):
+ *
+ *   k   [pages][heads][page / 16][head / C][16 tokens][C]  a cell is C values of one token
+ *   v   [pages][heads][page / C][head][C]                  a cell is C tokens' values of one column
+ *   ks, vs  u8 [pages][heads][page]                        e4m3 only
+ *
+ * moe_kv_layout_make fills *out [host] for 1 <= pages <= 2^24, page 16, 32,
+ * 64, 128 or 256, pages * page <= 2^30, 1 <= heads <= 256, head 64, 128 or
+ * 256, type MOE_BF16 or MOE_E4M3; MOE_ERR_INVALID otherwise.  Sections are
+ * 256-byte aligned.  Host only.
+ */
+typedef struct {
+    int32_t pages, page, heads, head, type, reserved;
+    uint64_t k, v, ks, vs;   /* byte offsets of the sections (ks, vs: 0 for bf16) */
+    uint64_t bytes;          /* size of the whole cache */
+} moe_kv_layout;
+moe_status moe_kv_layout_make(int32_t pages, int32_t page, int32_t heads, int32_t head, int32_t type,
+                              moe_kv_layout *out);
+
+/*
+ * Block tables and slots of one step.  Sequence s has length[s] tokens in
+ * the cache, in the pages table[s][0 .. ceil(length[s] / page) - 1], and
+ * gains grow[s] rows; grow[s] < 0 means that it is finished.
+ *
+ *   1. the pages of the finished sequences, in order, are put on top of the
+ *      stack of free pages (free_pages, *free_n of them); their length is 0
+ *   2. rows are numbered by sequence: starts[s + 1] = starts[s] + rows of s,
+ *      as far as they are below t
+ *   3. each page that the rows need is taken off the top of the stack, in
+ *      the order of the rows, and entered in the table
+ *
+ *   length, grow   [n]            read
+ *   table          [n][max_pages] entries, row stride ldt; new ones are written
+ *   free_pages     [L->pages], *free_n of them in use; pages given back are written
+ *   length_out     [n]      tokens after the step (may be `length` itself)
+ *   free_n_out     [1]      free pages after it (may be `free_n` itself)
+ *   starts         [n + 1]  first row of each sequence; starts[n] rows in all
+ *   positions      [t]      the row's position in its sequence (rows past starts[n]: 0)
+ *   slots          [t]      its slot, or -1: no free page or table entry was left, the
+ *                           table names a page that the cache lacks, or the row is past starts[n]
+ *   lacking        [1]      rows asked for (all grow[s] > 0) that have no slot, at most 2^31 - 1: 0 in a good step
+ * A sequence whose rows do not all have pages ends behind the last one that
+ * does (length_out).  Where length and free_n are not written in place, the
+ * step can then be planned again with fewer rows.  A length outside 0 ..
+ * max_pages * page counts as the nearest of these.  The kernel reads and
+ * writes nothing out of bounds whatever the integers are.
+ * Requires 1 <= n <= MOE_MAX_ROWS, 1 <= t <= MOE_MAX_ROWS, max_pages >= 1,
+ * max_pages * page <= 2^30, ldt >= max_pages.  No output may overlap an input
+ * or another output, but as said.
+ */
+moe_status moe_kv_plan(const int32_t *length, const int32_t *grow, int32_t n, int32_t t, const moe_kv_layout *L,
+                       int32_t *table, int32_t max_pages, int64_t ldt, int32_t *free_pages, const int32_t *free_n,
+                       int32_t *length_out, int32_t *free_n_out, int32_t *starts, int32_t *positions,
+                       int32_t *slots, int32_t *lacking, void *stream);
+
+/*
+ * Rows of new keys and values into the cache, rotated by their positions,
+ * and the queries rotated beside them:
+ *
+ *   (x_i, x_{i + rot/2}) -> (x_i c - x_{i + rot/2} s, x_{i + rot/2} c + x_i s),
+ *   c = rope[p][i], s = rope[p][rot/2 + i], p the row's position, i < rot/2
+ *
+ * for the first rot values of each head of k and q; the rest, and v, are
+ * stored as they are.  Each value is rounded once, to bf16, or to e4m3 with
+ * the smallest 2^E (-127 <= E <= 127) with max|x| <= 448 * 2^E over the head.
+ * An e4m3 value that is not finite becomes the code NaN and does not count
+ * towards the scale.
+ *
+ *   k, v       bf16 or fp32 (x_type) [t][heads * head], row strides ldk, ldv
+ *   slots      [t]; a row whose slot is outside 0 .. pages * page - 1 is not stored.
+ *              The slots of a call are distinct (or it is not said which row is kept)
+ *   positions  [t], rope fp32 [rope_rows][rot], 16-byte aligned; or both NULL and rot = 0:
+ *              nothing is rotated.  A position outside 0 .. rope_rows - 1 gives NaN for the
+ *              rotated values
+ *   q, q_out   x_type [t][heads_q * head], row stride ldq, and bf16 of row stride ldqo,
+ *              which may be q itself (bf16, equal strides); or both NULL.  Rows whose slot
+ *              is negative are left as they are.  Need rope
+ * Rows that are read or written start 16-byte aligned, at most 2^22 elements
+ * apart.  Requires 1 <= t <= MOE_MAX_ROWS, rot a multiple of 16 up to head,
+ * heads_q a multiple of heads up to 1024.  The cache must not overlap
+ * anything else, q_out nothing but q.
+ */
+moe_status moe_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t x_type, int32_t t,
+                         const moe_kv_layout *L, void *cache, const int32_t *slots, const int32_t *positions,
+                         const float *rope, int32_t rope_rows, int32_t rot, const void *q, int64_t ldq,
+                         int32_t heads_q, uint16_t *q_out, int64_t ldqo, void *stream);
+
+/*
+ * Bytes of the workspace of moe_attention_decode and moe_attention_prefill
+ * for t rows of n sequences and heads_q query heads on this cache.  It needs
+ * no initial value; calls that may run
+ * at the same time (on other streams, in other graphs) need one each.
+ * Returns 0 for invalid arguments.  Host only.
+ */
+size_t moe_attention_workspace_bytes(int32_t t, int32_t n, int32_t heads_q, const moe_kv_layout *L);
+
+/*
+ * Attention of one row per sequence over its length[s] tokens:
+ *
+ *   out[r][h] = sum_j p_j v_j,  p = softmax_j(scale * q[r][h] . k_j),  0 <= j < length[s]
+ *
+ * where query head h reads key head h / (heads_q / heads).  Token j is in
+ * page table[s][j / page].  A length outside 0 .. max_pages * page counts as
+ * the nearest of these, and tokens of pages that the cache lacks (entries
+ * outside 0 .. pages - 1) as not there.  A row without any token is 0.
+ * Tokens that are not there, whatever their bytes hold, reach no output.
+ *
+ *   q      bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
+ *   starts NULL: row s is sequence s's, t = n.  Else [n + 1], ascending, 0 .. t: the row of
+ *          sequence s is the last of starts[s] .. starts[s + 1] - 1; sequences without
+ *          rows are passed over, other rows left as they are
+ *   table  [n][max_pages], row stride ldt;  length [n];  scale > 0, finite
+ * Rows 16-byte aligned, at most 2^22 elements apart; out must not overlap
+ * anything else.  Requires 1 <= t, n <= MOE_MAX_ROWS, heads_q a multiple of
+ * heads up to 1024, max_pages * page <= 2^30; MOE_ERR_WORKSPACE for a
+ * workspace smaller than moe_attention_workspace_bytes(t, n, heads_q, L).
+ * Scores, softmax and sums are fp32; the result is bitwise the same for the
+ * same arguments.
+ */
+moe_status moe_attention_decode(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                int32_t max_pages, int64_t ldt, const int32_t *length, float scale, uint16_t *out,
+                                int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Causal attention of a chunk's packed rows.  Rows starts[s] .. starts[s + 1]
+ * - 1 are the last tokens of sequence s, which has length[s] of them in the
+ * cache (the rows' own among them): with m rows, its row i sits at position
+ * p = length[s] - m + i and reads the tokens 0 <= j <= p.  A row with p < 0
+ * is 0; rows that belong to no sequence are left as they are.
+ *
+ *   q       bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
+ *   starts  [n + 1], ascending, 0 .. t;  the rest as for moe_attention_decode
+ * The weights p_j are rounded to bf16 (relative to the row's largest) before
+ * they meet v; scores, softmax and sums are fp32.  Requires 1 <= t <=
+ * MOE_MAX_ROWS and a workspace of moe_attention_workspace_bytes(t, n, heads_q, L).
+ */
+moe_status moe_attention_prefill(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                 int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                 int32_t max_pages, int64_t ldt, const int32_t *length, float scale, uint16_t *out,
+                                 int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

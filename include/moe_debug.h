@@ -49,7 +49,9 @@ enum {
     MOE_PHASE_NORM = 9,        /* injection into the residual copies and the next norm; moe_residual_norm */
     MOE_PHASE_EXPERTS = 10,    /* routed grouped gate/up + SiLU*up and down in one launch */
     MOE_PHASE_LINEAR = 11,     /* moe_linear and moe_linear_gated */
-    MOE_PHASES = 12
+    MOE_PHASE_KV = 12,         /* moe_kv_plan and moe_kv_append */
+    MOE_PHASE_ATTENTION = 13,  /* moe_attention_decode and moe_attention_prefill */
+    MOE_PHASES = 14
 };
 void moe_profile_begin(uint32_t mask);
 int moe_profile_end(double *ms, int64_t *launches);

@@ -57,6 +57,12 @@ class moe_matrix_layout(ctypes.Structure):
                 ("w", ctypes.c_uint64), ("sb", ctypes.c_uint64), ("bytes", ctypes.c_uint64)]
 
 
+class moe_kv_layout(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page", ctypes.c_int32), ("heads", ctypes.c_int32), ("head", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k", ctypes.c_uint64), ("v", ctypes.c_uint64),
+                ("ks", ctypes.c_uint64), ("vs", ctypes.c_uint64), ("bytes", ctypes.c_uint64)]
+
+
 class moe_ring_stats(ctypes.Structure):
     _fields_ = [("jobs", ctypes.c_int32), ("streamed", ctypes.c_int32), ("batches", ctypes.c_int32),
                 ("fetched_bytes", ctypes.c_uint64), ("wait_ms", ctypes.c_double)]
@@ -70,10 +76,11 @@ EXPORTS = ["moe_last_error", "moe_layout_make", "moe_workspace_bytes", "moe_rout
            "moe_layout_make_bits", "moe_ring_set_miss_layout", "moe_residency", "moe_lookahead",
            "moe_block_from_residual", "moe_chunk_stats_fill", "moe_debug_read_probe",
            "moe_debug_schedule", "moe_debug_xcc_map", "moe_debug_tile_wait", "moe_matrix_layout_make",
-           "moe_linear", "moe_linear_gated", "moe_residual_norm"]
+           "moe_linear", "moe_linear_gated", "moe_residual_norm", "moe_kv_layout_make", "moe_kv_plan",
+           "moe_kv_append", "moe_attention_workspace_bytes", "moe_attention_decode", "moe_attention_prefill"]
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 PHASES = ["router", "topk", "csr", "shared_gateup", "shared_down", "schedule", "gateup", "down", "combine", "norm",
-          "experts", "linear"]  # MOE_PHASE_* in order; moe_profile_end fills one entry each
+          "experts", "linear", "kv", "attention"]  # MOE_PHASE_* in order; moe_profile_end fills one entry each
 
 
 def lib():
@@ -124,6 +131,14 @@ def lib():
     L.moe_linear.argtypes = [P, I, Q, P, I, I, MP, P, P, I, Q, I, P]
     L.moe_linear_gated.argtypes = [P, I, Q, P, I, I, MP, P, P, P, I, Q, P, P]
     L.moe_residual_norm.argtypes = [P, I, Q, P, P, I, Q, P, ctypes.c_float, I, I, P, Q, P, Q, P, I, P]
+    KP = ctypes.POINTER(moe_kv_layout)
+    L.moe_kv_layout_make.argtypes = [I, I, I, I, I, KP]
+    L.moe_kv_plan.argtypes = [P, P, I, I, KP, P, I, Q, P, P, P, P, P, P, P, P, P]
+    L.moe_kv_append.argtypes = [P, Q, P, Q, I, I, KP, P, P, P, P, I, I, P, Q, I, P, Q, P]
+    L.moe_attention_workspace_bytes.argtypes = [I, I, I, KP]
+    L.moe_attention_workspace_bytes.restype = Z
+    L.moe_attention_decode.argtypes = [P, Q, P, I, I, I, KP, P, P, I, Q, P, ctypes.c_float, P, Q, P, Z, P]
+    L.moe_attention_prefill.argtypes = [P, Q, P, I, I, I, KP, P, P, I, Q, P, ctypes.c_float, P, Q, P, Z, P]
     L.moe_ring_plan_debug.argtypes = [P, P, I, I, I, P, P, P]
     L.moe_profile_begin.argtypes = [ctypes.c_uint32]
     L.moe_profile_begin.restype = None
@@ -134,7 +149,8 @@ def lib():
     for f in ("moe_layout_make", "moe_layout_make_bits", "moe_ring_set_miss_layout", "moe_route", "moe_build_csr", "moe_shared", "moe_ring_create",
               "moe_ring_get_stats", "moe_prefill_experts", "moe_prefill_fused", "moe_block", "moe_block_noalloc", "moe_inject_norm", "moe_block_next_norm",
               "moe_residency", "moe_lookahead", "moe_block_from_residual", "moe_chunk_stats_fill",
-              "moe_matrix_layout_make", "moe_linear", "moe_linear_gated", "moe_residual_norm"):
+              "moe_matrix_layout_make", "moe_linear", "moe_linear_gated", "moe_residual_norm", "moe_kv_layout_make",
+              "moe_kv_plan", "moe_kv_append", "moe_attention_decode", "moe_attention_prefill"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
@@ -570,6 +586,141 @@ def moe_residual_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual
              _flat(gamma, h, dev, "gamma"), eps, t, h, op, ldo, cp, ldc, sp, sk)
 
 
+# ------------------------------------------------------------------ attention over a paged key-value cache
+# Rows as for the layer operators; lengths, tables, slots and the like are int32.
+
+def moe_kv_layout_make(pages: int, page: int, heads: int, head: int, dtype: torch.dtype = torch.bfloat16) -> moe_kv_layout:
+    """A cache of `pages` pages of `page` tokens for `heads` key heads of `head` values, bfloat16 or float8_e4m3fn."""
+    out = moe_kv_layout()
+    _check(lib().moe_kv_layout_make(pages, page, heads, head, _ROW_TYPES.get(dtype, -1), ctypes.byref(out)))
+    return out
+
+
+def _ints(x: torch.Tensor, n: int, dev: int, what: str) -> int:
+    """The pointer of n contiguous int32 on GPU `dev`."""
+    if x.dtype != torch.int32:
+        raise ValueError(f"{what} must be int32, not {x.dtype}")
+    return _flat(x, n, dev, what)
+
+
+def _table_args(table: torch.Tensor, n: int, dev: int):
+    """(pointer, entries a row, row stride) of the page tables of n sequences."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n or table.shape[1] < 1:
+        raise ValueError(f"table must be an int32 [{n}, pages] tensor, not {table.dtype} {list(table.shape)}")
+    ld, step = table.stride()
+    width = table.shape[1]
+    if (step != 1 and width > 1) or (n > 1 and ld < width):
+        raise ValueError("table needs a contiguous last dimension and rows that do not overlap")
+    if table.get_device() != dev:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    return table.data_ptr(), width, ld if n > 1 else width
+
+
+def _cache(cache: torch.Tensor, layout: moe_kv_layout, dev: int) -> int:
+    """The pointer of a cache of this layout on GPU `dev`."""
+    if not cache.is_contiguous() or cache.numel() * cache.element_size() < layout.bytes:
+        raise ValueError(f"a cache of this layout is {layout.bytes} contiguous bytes")
+    if cache.get_device() != dev:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    return cache.data_ptr()
+
+
+def _heads_of(q: torch.Tensor, layout: moe_kv_layout, what: str) -> int:
+    if q.dim() != 2 or q.shape[1] < 1 or q.shape[1] % layout.head:
+        raise ValueError(f"{what} must be [rows, heads * {layout.head}], not {list(q.shape)}")
+    return q.shape[1] // layout.head
+
+
+def moe_kv_plan(length: torch.Tensor, grow: torch.Tensor, layout: moe_kv_layout, table: torch.Tensor,
+                free_pages: torch.Tensor, free_n: torch.Tensor, length_out: torch.Tensor, free_n_out: torch.Tensor,
+                starts: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, lacking: torch.Tensor,
+                stream=None) -> None:
+    """Pages, positions and slots of a step in which sequence s gains grow[s] rows (-1: it is finished and its pages
+    become free): length, grow [n], table [n, pages], free_pages [layout.pages] with free_n [1] of them in use ->
+    length_out [n] (may be length), free_n_out [1] (may be free_n), starts [n + 1], positions and slots [t],
+    lacking [1] (rows without a slot)."""
+    dev, n, t = length.get_device(), length.numel(), positions.numel()
+    if dev < 0:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    tp, width, ldt = _table_args(table, n, dev)
+    _call_on(dev, stream, (_lib or lib()).moe_kv_plan, _ints(length, n, dev, "length"), _ints(grow, n, dev, "grow"), n, t,
+             ctypes.byref(layout), tp, width, ldt, _ints(free_pages, layout.pages, dev, "free_pages"),
+             _ints(free_n, 1, dev, "free_n"), _ints(length_out, n, dev, "length_out"),
+             _ints(free_n_out, 1, dev, "free_n_out"), _ints(starts, n + 1, dev, "starts"),
+             _ints(positions, t, dev, "positions"), _ints(slots, t, dev, "slots"), _ints(lacking, 1, dev, "lacking"))
+
+
+def moe_kv_append(k: torch.Tensor, v: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows k and v [t, heads * head] (bfloat16 or float32) into the cache at slots [t]; with rope float32
+    [positions, rot] (cosines, then sines) and positions [t], k turned by its position and q [t, heads_q * head] into
+    q_out (bfloat16, may be q)."""
+    dev, t, width = k.get_device(), k.shape[0], layout.heads * layout.head
+    kp, xt, ldk = _row_args(k, t, width, dev, "k")
+    vp, vt, ldv = _row_args(v, t, width, dev, "v")
+    qp, qt, ldq, qop, qot, ldqo, hq = None, xt, 0, None, BF16, 0, 0
+    if q is not None:
+        hq = _heads_of(q, layout, "q")
+        qp, qt, ldq = _row_args(q, t, hq * layout.head, dev, "q")
+    if q_out is not None:
+        qop, qot, ldqo = _row_args(q_out, t, (hq or 1) * layout.head, dev, "q_out")
+    if vt != xt or qt != xt or qot != BF16:
+        raise ValueError("k, v and q must have one type, q_out is bfloat16")
+    rp, rows, rot = None, 0, 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype != torch.float32:
+            raise ValueError("rope must be float32 [positions, rot]")
+        rows, rot = rope.shape
+        rp = _flat(rope, rows * rot, dev, "rope")
+    _call_on(dev, stream, (_lib or lib()).moe_kv_append, kp, ldk, vp, ldv, xt, t, ctypes.byref(layout),
+             _cache(cache, layout, dev), _ints(slots, t, dev, "slots"),
+             None if positions is None else _ints(positions, t, dev, "positions"), rp, rows, rot, qp, ldq, hq, qop, ldqo)
+
+
+def moe_attention_workspace_bytes(t: int, n: int, heads_q: int, layout: moe_kv_layout) -> int:
+    return lib().moe_attention_workspace_bytes(t, n, heads_q, ctypes.byref(layout))
+
+
+def _attention_args(q, layout, cache, table, n, length, out, workspace):
+    dev, t, hq = q.get_device(), q.shape[0], _heads_of(q, layout, "q")
+    qp, qt, ldq = _row_args(q, t, hq * layout.head, dev, "q")
+    op, ot, ldo = _row_args(out, t, hq * layout.head, dev, "out")
+    if qt != BF16 or ot != BF16:
+        raise ValueError("q and out must be bfloat16")
+    tp, width, ldt = _table_args(table, n, dev)
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous, on the GPU of the other tensors")
+    return (dev, t, hq, qp, ldq, _cache(cache, layout, dev), tp, width, ldt, _ints(length, n, dev, "length"), op, ldo,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def moe_attention_decode(q: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor, table: torch.Tensor,
+                         length: torch.Tensor, scale: float, out: torch.Tensor, workspace: torch.Tensor,
+                         starts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out [t, heads_q * head] = attention of one row a sequence, q [t, heads_q * head] bfloat16, over its first
+    length[s] tokens: row s, or with starts [n + 1] the last of rows starts[s] .. starts[s + 1] - 1, if any;
+    workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes."""
+    n = length.numel()
+    dev, t, hq, qp, ldq, cp, tp, width, ldt, lp, op, ldo, wp, wn = _attention_args(
+        q, layout, cache, table, n, length, out, workspace)
+    _call_on(dev, stream, (_lib or lib()).moe_attention_decode, qp, ldq,
+             None if starts is None else _ints(starts, n + 1, dev, "starts"), t, n, hq, ctypes.byref(layout), cp, tp, width,
+             ldt, lp, scale, op, ldo, wp, wn)
+
+
+def moe_attention_prefill(q: torch.Tensor, starts: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor,
+                          table: torch.Tensor, length: torch.Tensor, scale: float, out: torch.Tensor,
+                          workspace: torch.Tensor, stream=None) -> None:
+    """Causal attention of the packed rows q [t, heads_q * head], rows starts[s] .. starts[s + 1] - 1 being the last
+    of the length[s] tokens of sequence s; workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes."""
+    n = length.numel()
+    dev, t, hq, qp, ldq, cp, tp, width, ldt, lp, op, ldo, wp, wn = _attention_args(
+        q, layout, cache, table, n, length, out, workspace)
+    _call_on(dev, stream, (_lib or lib()).moe_attention_prefill, qp, ldq, _ints(starts, n + 1, dev, "starts"), t, n, hq,
+             ctypes.byref(layout), cp, tp, width, ldt, lp, scale, op, ldo, wp, wn)
+
+
 def moe_ring_plan_debug(offsets, resident, n_slots: int = 64, group: int = 8):
     """Host-only ring schedule (numpy in, numpy out): slot[E], batch[E], wait[batches]."""
     import numpy as np
@@ -614,3 +765,4 @@ def moe_profile_end() -> dict:
 
 from .block import MoeBlock  # noqa: E402  (device-buffer owner built on the calls above)
 from .matrix import MoeMatrix  # noqa: E402
+from .cache import MoeCache  # noqa: E402
