@@ -754,8 +754,8 @@ moe_status moe_attention_decode(const uint16_t *q, int64_t ldq, const int32_t *s
  *
  *   q       bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
  *   starts  [n + 1], ascending, 0 .. t;  the rest as for moe_attention_decode
- * The weights p_j are rounded to bf16 (relative to the row's largest) before
- * they meet v; scores, softmax and sums are fp32.  Requires 1 <= t <=
+ * The weights p_j are rounded to bf16 before they are summed and meet v;
+ * scores, softmax and sums are fp32.  Requires 1 <= t <=
  * MOE_MAX_ROWS and a workspace of moe_attention_workspace_bytes(t, n, heads_q, L).
  */
 moe_status moe_attention_prefill(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,

@@ -23,6 +23,7 @@
 namespace moe {
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -63,6 +64,7 @@ struct Unit {
     int s, len, rows, first;  // the sequence, its tokens, its rows and the first of them
     int tile, split, part;    // part of the `split` parts of the tile's tokens
     int slot;                 // where its partial result goes (split > 1)
+    int cuts;                 // partial results of the head in all
 };
 
 // One sequence as the units see it.
@@ -123,7 +125,8 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
         const int s = __builtin_ctzll(past);
         auto get = [&](int x) { return __builtin_amdgcn_readlane(x, s); };
         const int at = v - get(ue - units), n_s = get(n), tiles = get(q.tiles);
-        u = Unit{s, get(q.len), get(q.rows), get(q.first), tiles - 1 - at / n_s, n_s, at % n_s, get(pe - parts)};
+        u = Unit{s, get(q.len), get(q.rows), get(q.first), tiles - 1 - at / n_s, n_s, at % n_s, get(pe - parts),
+                 __builtin_amdgcn_readlane(pe, 63)};
     } else {
         __shared__ int64_t wave_work[4];
         __shared__ int wave_units[4], wave_parts[4];
@@ -139,7 +142,9 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
         if (lane == 0) wave_work[wave] = work;
         if (tid == 0) found.s = -1;
         __syncthreads();
-        const int tokens = part_tokens<PREFILL>(wave_work[0] + wave_work[1] + wave_work[2] + wave_work[3], heads);
+        work = 0;
+        for (int w = 0; w < 4; ++w) work += wave_work[w];
+        const int tokens = part_tokens<PREFILL>(work, heads);
         int units = 0, parts = 0;
         for (int s = s0; s < s1; ++s) {
             const Seq q = seq_of<PREFILL>(a, s, group);
@@ -164,7 +169,7 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
                 const int n = splits(q, tokens);
                 if (v < ub + q.tiles * n) {
                     const int at = v - ub;
-                    found = Unit{s, q.len, q.rows, q.first, q.tiles - 1 - at / n, n, at % n, pb};
+                    found = Unit{s, q.len, q.rows, q.first, q.tiles - 1 - at / n, n, at % n, pb, 0};
                     break;
                 }
                 ub += q.tiles * n;
@@ -174,15 +179,19 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
         __syncthreads();
         u = found;
         if (u.s < 0) return false;
+        u.cuts = 0;
+        for (int w = 0; w < 4; ++w) u.cuts += wave_parts[w];
     }
     // the tiles of a sequence run from its last, which have the most tokens; slots are in the order of the tiles
     u.slot += u.tile * u.split + u.part;
     return true;
 }
 
-// What the joining launch has to know of a sequence, from its first unit.
+// What the joining launch has to know, of a sequence from its first unit, and
+// whether there is anything to join from the call's first.
 __device__ __forceinline__ void leave_info(const AttentionArgs &a, const Unit &u, int head_tile) {
     if (threadIdx.x == 0 && head_tile == 0 && u.tile == 0 && u.part == 0) a.info[u.s] = make_int2(u.split, u.slot);
+    if (threadIdx.x == 0 && blockIdx.x == 0) a.info[a.n] = make_int2(u.cuts, 0);
 }
 
 // ------------------------------------------------------------------ one row a sequence
@@ -395,9 +404,17 @@ __global__ void __launch_bounds__(256) k_decode(AttentionArgs a) {
 
 // ------------------------------------------------------------------ packed rows
 
-// 16 bytes a lane from memory to LDS byte `to` + 16 lane.
-__device__ __forceinline__ void dma16(uint32_t to, const void *from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(from) : "memory", "m0");
+// 16 bytes a lane from memory to LDS byte `to` + 16 lane (the instruction adds
+// its offset to both addresses).
+__device__ __forceinline__ void dma16(uint32_t to, const void *from, int offset) {  // offset: a constant below 4096
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+                 : : "s"(to - offset), "v"(from), "i"(offset) : "memory", "m0");
+}
+
+// The same from a uniform address and an offset a lane.
+__device__ __forceinline__ void dma16(uint32_t to, const void *from, uint32_t lane_offset, int offset) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
+                 : : "s"(to - offset), "v"(lane_offset), "s"(from), "i"(offset) : "memory", "m0");
 }
 
 // Whether any bf16 of a cell is an infinity or NaN.
@@ -413,15 +430,18 @@ __device__ __forceinline__ bool not_finite(u32x4 w) {
 // them, over a run of the sequence's tokens, in tiles of TK tokens that the
 // four waves share in LDS: the cells of the cache as they are (e4m3: widened
 // to bf16 on the way), which is the order in which the 32x32x16 products read
-// them, 16 bytes a lane without bank conflicts.  The next tile is on its way
-// while one is computed.  Rows of a short chunk fill the tile with the heads
-// that share their keys.
+// them, 16 bytes a lane without bank conflicts.  Rows of a short chunk fill
+// the tile with the heads that share their keys.
+//
+// A wave computes the scores of tile t + 1 while it turns those of tile t into
+// weights, so that the matrix core and the vector units are both busy; keys
+// are therefore fetched two tiles ahead, values one.
 template <int CT, int D, bool SMALL>
-__global__ void __launch_bounds__(256, 2) k_prefill(AttentionArgs a) {
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;
-    constexpr int TK = D == 256 ? 32 : 64, TB = TK * D * 2;  // tokens a tile, bytes of its keys (or values)
+    constexpr int TK = D == 256 && E4M3 ? 32 : 64, TB = TK * D * 2;  // tokens a tile, bytes of its keys (or values)
     constexpr int NB = TK / 32, NKS = D / 16, NVS = TK / 16, ND = D / 32;
-    __shared__ __align__(16) uint8_t tile_lds[4 * TB];  // [2][keys, values]
+    __shared__ __align__(16) uint8_t tile_lds[4 * TB];  // keys [2], values [2]
     const KvCache &c = a.c;
     const int G = a.heads_q / c.heads, H = c.heads, h = blockIdx.x % H;
     Unit u;
@@ -431,18 +451,16 @@ __global__ void __launch_bounds__(256, 2) k_prefill(AttentionArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(tile_lds));
 
-    // the lane's row: pair x of the sequence, token x / G, query head x % G; its position
-    const int pairs = u.rows * G, x0 = u.tile * kPrefillRows, before = u.len - u.rows;
-    const int x = x0 + wave * 32 + m, token = x / G;
-    const bool live = x < pairs;
-    const int pos = live ? before + token : 1 << 30;
-    const bool wave_live = x0 + wave * 32 < pairs;
-    const int wave_min = before + (x0 + wave * 32) / G, wave_max = before + min(x0 + wave * 32 + 31, pairs - 1) / G;
+    // the lane's rows: pair x of the sequence, token x / G, query head x % G; their positions
+    const int pairs = u.rows * G, x0 = u.tile * kPrefillRows, xw = x0 + wave * 32, before = u.len - u.rows;
+    const bool wave_live = xw < pairs;
+    const int wave_min = before + xw / G, wave_max = before + min(xw + 31, pairs - 1) / G;
     const int tile_min = before + x0 / G, tile_end = max(before + min(x0 + kPrefillRows - 1, pairs - 1) / G + 1, 0);
     const int tiles = (tile_end + TK - 1) / TK, each = (tiles + u.split - 1) / u.split;
     const int t0 = u.part * each, t1 = min(t0 + each, tiles);
-
-    const size_t out_at = live ? (size_t)(u.first + token) * a.ldo + (size_t)(h * G + x % G) * D : 0;
+    const int x = xw + m, token = x / G;
+    const bool live = x < pairs;
+    const int pos = live ? before + token : 1 << 30;
     bf16x8 qf[NKS];
     {
         const uint16_t *q = a.q + (live ? (size_t)(u.first + token) * a.ldq + (size_t)(h * G + x % G) * D : 0);
@@ -461,217 +479,347 @@ __global__ void __launch_bounds__(256, 2) k_prefill(AttentionArgs a) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
 
-    const int page_mask = (1 << c.shift) - 1, key = lane & (TK - 1);
+    // Tile kt's token `key` is token (kt TK & mask) + (key & mask) of the page of entry (kt TK >> shift) + (key >> shift).
+    constexpr int SIZE = E4M3 ? 1 : 2;
+    const int page_mask = (1 << c.shift) - 1, key = lane & (TK - 1), in_page = key & page_mask;
     const int32_t *row = a.table + u.s * a.ldt;
     auto entry = [&](int kt) {  // page of the lane's token of a tile, -1: none
-        const int tok = kt * TK + key;
-        const int p = kt < t1 && tok < u.len ? row[tok >> c.shift] : -1;
+        const int32_t *at = row + (kt * TK >> c.shift);
+        const int p = kt < t1 && kt * TK + key < u.len ? at[key >> c.shift] : -1;
         return (unsigned)p < (unsigned)c.pages ? p : -1;
     };
-    // byte offset of (page, head, token in the page) cells of w bytes a token; page -1: page 0, whose bytes are not used
-    auto place = [&](int e, int in, int w) { return ((((size_t)max(e, 0) * H + h) << c.shift) + in) * w; };
-    // bf16: the tile on its way into buffer `buf`
-    auto fetch = [&](int kt, int e, int buf) {
-        constexpr int NI = TB / 1024 / 4;  // loads a wave, of keys and of values
-        const int tok = kt * TK + key;
-        const uint8_t *kp = c.k + place(e, tok & page_mask & ~15, D * 2) + (tok & 15) * 16;
-        const uint32_t to = lds0 + buf * 2 * TB;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int at = wave * NI + i, chunk = TK == 64 ? at : 2 * at + hf;
-            dma16(to + at * 1024, kp + chunk * 256);
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int at = wave * NI + i, group = at * 64 / D, in = at * 64 % D;
-            const int eg = __builtin_amdgcn_readlane(e, 8 * group);
-            const uint8_t *vp = c.v + place(eg, (kt * TK + 8 * group) & page_mask, D * 2) + in * 16;
-            dma16(to + TB + at * 1024, vp + lane * 16);
-        }
+    // a head's cells in page p start p * page_bytes further (p = -1: in page 0, whose bytes are not used)
+    const uint32_t page_bytes = (uint32_t)(H << c.shift) * (D * SIZE);
+    const uint8_t *const k_head = c.k + (h << c.shift) * (D * SIZE), *const v_head = c.v + (h << c.shift) * (D * SIZE);
+    auto cells = [&](const uint8_t *head, int p) { return head + (uint64_t)(uint32_t)max(p, 0) * page_bytes; };
+    auto tile_offset = [&](int kt) { return (uint32_t)(kt * TK & page_mask) * (D * SIZE); };
+    auto keys_at = [&](int kt) { return (kt & 1) * TB; };
+    auto values_at = [&](int kt) { return (2 + (kt & 1)) * TB; };
+    // bf16: a tile's keys (values) on their way into LDS, NI loads a wave, load i of them; the lane's address is that
+    // of the first (values: of the first of each group of 8 tokens)
+    constexpr int NI = TB / 1024 / 4, GROUPS = NI * 64 > D ? NI * 64 / D : 1;
+    const uint8_t *const k_mine = k_head + (in_page & ~15) * (D * 2) + (key & 15) * 16 + (TK == 64 ? wave * NI : 2 * wave * NI + hf) * 256;
+    auto keys_from = [&](int kt, int e) { return cells(k_mine, e) + tile_offset(kt); };
+    auto values_from = [&](int kt, int e, int i) {
+        const int at = (wave * NI + i * (D / 64)) * 64, group = at / D;
+        return cells(v_head, __builtin_amdgcn_readlane(e, 8 * group)) + tile_offset(kt) + (8 * group & page_mask) * (D * 2) + at % D * 16;
     };
-    // e4m3: the tile's codes into registers, later widened into buffer `buf`
-    constexpr int NC = E4M3 ? TK * D / 16 / 256 : 1;  // cells a thread, of keys and of values
+    const uint32_t lds_wave = lds0 + wave * NI * 1024;
+    auto fetch_keys = [&](int kt, const uint8_t *from, int i) {
+        dma16(lds_wave + keys_at(kt) + i * 1024, from, i * (TK == 64 ? 256 : 512));
+    };
+    auto fetch_values = [&](int kt, const uint8_t *const (&from)[GROUPS], int i) {
+        dma16(lds_wave + values_at(kt) + i * 1024, from[i / (D / 64)], lane * 16, i % (D / 64) * 1024);
+    };
+    // e4m3: a tile's codes into registers, later widened into LDS
+    constexpr int NC = E4M3 ? TK * D / 16 / 256 : 1;  // cells a thread
     u32x4 kc[NC], vc[NC], vsc[NC];
     uint32_t ksc[NC];
-    auto load = [&](int kt, int e) {
+    auto scales = [&](const uint8_t *all, int p) { return all + ((uint64_t)(uint32_t)max(p, 0) * (uint32_t)(H << c.shift) + (h << c.shift)); };
+    auto load_keys = [&](int kt, int e) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int cell = tid + 256 * i, chunk = cell / TK, tok = kt * TK + key;  // cell % TK == key
-            kc[i] = *reinterpret_cast<const u32x4 *>(c.k + place(e, tok & page_mask & ~15, D) + chunk * 256 + (tok & 15) * 16);
-            ksc[i] = c.ks[place(e, tok & page_mask, 1)];
-            const int group = __builtin_amdgcn_readfirstlane(cell / D), col = cell % D;
-            const int eg = __builtin_amdgcn_readlane(e, 16 * group), in = (kt * TK + 16 * group) & page_mask;
-            vc[i] = *reinterpret_cast<const u32x4 *>(c.v + place(eg, in, D) + col * 16);
-            vsc[i] = *reinterpret_cast<const u32x4 *>(c.vs + place(eg, in, 1));
+            const int chunk = (tid + 256 * i) / TK;  // the cell's token is the lane's
+            kc[i] = *reinterpret_cast<const u32x4 *>(cells(k_head, e) + tile_offset(kt) + (in_page & ~15) * D + (key & 15) * 16 + chunk * 256);
+            ksc[i] = scales(c.ks, e)[(kt * TK & page_mask) + in_page];
         }
     };
-    auto widen = [&](int buf) {
-        uint8_t *kb = tile_lds + buf * 2 * TB, *vb = kb + TB;
+    auto load_values = [&](int kt, int e) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int cell = tid + 256 * i, chunk = cell / TK, group = cell / D, col = cell % D;
-            const float f = scale_of(ksc[i], 0);
-            *reinterpret_cast<bf16x8 *>(kb + (2 * chunk * TK + key) * 16) = e4m3_bf16(kc[i].x, kc[i].y, f);
-            *reinterpret_cast<bf16x8 *>(kb + ((2 * chunk + 1) * TK + key) * 16) = e4m3_bf16(kc[i].z, kc[i].w, f);
-            u32x4 w[2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vc[i][j], 1.0f, false);
-                const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vc[i][j], 1.0f, true);
-                const uint32_t a0 = __builtin_bit_cast(uint32_t, p0), a1 = __builtin_bit_cast(uint32_t, p1);
-                // a power of two each: exact
-                w[j / 2][j % 2 * 2] = pk_bf16(bf16_lo(a0) * scale_of(vsc[i][j], 0), bf16_hi(a0) * scale_of(vsc[i][j], 1));
-                w[j / 2][j % 2 * 2 + 1] = pk_bf16(bf16_lo(a1) * scale_of(vsc[i][j], 2), bf16_hi(a1) * scale_of(vsc[i][j], 3));
-            }
-            *reinterpret_cast<u32x4 *>(vb + (2 * group * D + col) * 16) = w[0];
-            *reinterpret_cast<u32x4 *>(vb + ((2 * group + 1) * D + col) * 16) = w[1];
+            const int cell = tid + 256 * i, group = __builtin_amdgcn_readfirstlane(cell / D), col = cell % D;
+            const int eg = __builtin_amdgcn_readlane(e, 16 * group), in = (kt * TK & page_mask) + (16 * group & page_mask);
+            vc[i] = *reinterpret_cast<const u32x4 *>(cells(v_head, eg) + in * D + col * 16);
+            vsc[i] = *reinterpret_cast<const u32x4 *>(scales(c.vs, eg) + in);
         }
+    };
+    // widened in pieces of about eight instructions, six a cell: a half of its keys twice, a quarter of its values four times
+    constexpr int PIECES = E4M3 ? 6 * NC : 0;
+    constexpr bool BETWEEN = D == 256;  // between the products: one wave a SIMD has nothing else to fill them with
+    u32x4 wide;
+    auto widen = [&](int keys, int values, int y) {  // tile `keys` and tile `values`
+        const int i = y / 6, part = y % 6, cell = tid + 256 * i;
+        if (part < 2) {
+            uint8_t *kb = tile_lds + keys_at(keys) + (2 * (cell / TK) * TK + key) * 16;
+            *reinterpret_cast<bf16x8 *>(kb + part * TK * 16) = e4m3_bf16(kc[i][2 * part], kc[i][2 * part + 1], scale_of(ksc[i], 0));
+            return;
+        }
+        const int j = part - 2;
+        const f32x2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8(vc[i][j], false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8(vc[i][j], true);
+        // a power of two each: exact; the wave's tokens are the same 16
+        const uint32_t f = __builtin_amdgcn_readfirstlane(vsc[i][j]);
+        wide[j % 2 * 2] = pk_bf16(p0.x * scale_of(f, 0), p0.y * scale_of(f, 1));
+        wide[j % 2 * 2 + 1] = pk_bf16(p1.x * scale_of(f, 2), p1.y * scale_of(f, 3));
+        if (j % 2)
+            *reinterpret_cast<u32x4 *>(tile_lds + values_at(values) + ((2 * (cell / D) + j / 2) * D + cell % D) * 16) = wide;
     };
 
     // a lane's row of K: bits 2 and 3 of its number swapped, so that the lane's 16 scores of a block are 8 + 8 neighbours
     const int krow = (m & 0x13) | (m & 4) << 1 | (m & 8) >> 1;
     constexpr uint64_t ALL = TK == 64 ? ~0ull : (1ull << 32) - 1;
-    int e = entry(t0);
-    uint64_t there = __ballot(e >= 0) & ALL, there_next = 0;  // the tile's tokens that are there
-    if (t0 < t1) {
-        if (E4M3) {
-            load(t0, e);
-            widen(0);
-        } else {
-            fetch(t0, e, 0);
+    typedef f32x16 Scores[NB];
+    // operand x of a tile's products, in their order: of the scores (block of 32 tokens, 16 columns), of the outputs
+    // (16 tokens, block of 32 columns)
+    constexpr int NK = NB * NKS, NV = NVS * ND;
+    const uint8_t *const k_lane = tile_lds + (hf * TK + krow) * 16, *const v_lane = tile_lds + 2 * TB + (hf * D + m) * 16;
+    auto key_frag = [&](int kt, int x) {
+        return *reinterpret_cast<const bf16x8 *>(k_lane + (kt & 1) * TB + x % NKS * (2 * TK * 16) + x / NKS * 512);
+    };
+    auto value_frag = [&](int kt, int x) {
+        return *reinterpret_cast<const bf16x8 *>(v_lane + (kt & 1) * TB + x / ND * (2 * D * 16) + x % ND * 512);
+    };
+    auto zero = [&](Scores &s, int b) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[b][j] = 0.0f;
+    };
+    auto score = [&](Scores &s, const bf16x8 &kf, int x) {
+        s[x / NKS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x % NKS], s[x / NKS], 0, 0, 0);
+    };
+    // no score for tokens that are not there or come after the row (there: the tile's tokens that are)
+    auto mask = [&](Scores &s, int kt, uint64_t there) {
+        const int k0 = kt * TK;
+        if (there == ALL && k0 + TK - 1 <= wave_min) return;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            // bit i: the token 8 hf + i of the block may be read
+            const int last = pos - (k0 + 32 * b + 8 * hf);
+            uint32_t ok = (uint32_t)(there >> (32 * b + 8 * hf));
+            ok &= last < 0 ? 0u : last > 30 ? 0xffffffffu : (2u << last) - 1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (!(ok >> (j / 8 * 16 + j % 8) & 1)) s[b][j] = minus_inf();
         }
-    }
-    e = entry(t0 + 1);
-    for (int kt = t0; kt < t1; ++kt) {
-        const int buf = (kt - t0) & 1, k0 = kt * TK;
-        uint8_t *kb = tile_lds + buf * 2 * TB, *vb = kb + TB;
-        lds::wait_vm<0>();
-        lds::barrier_no_fence();  // the tile is in, and no wave reads the other buffer any more
-        const bool more = kt + 1 < t1;
-        if (more) {
-            there_next = __ballot(e >= 0) & ALL;
-            if (E4M3) load(kt + 1, e);
-            else fetch(kt + 1, e, buf ^ 1);
-            e = entry(kt + 2);
-        }
-        // A tile that some row does not read whole.  A weight of 0 does not
-        // keep an infinity or NaN in V out of the sum, so tokens that are not
-        // there become 0, and where a token that later rows read is not finite
-        // its column is added to those rows by hand.
-        bool by_hand = false;
-        if (there != ALL || k0 + TK - 1 > tile_min) {
-            bool bad = false;
-            for (int cell = tid; cell < TB / 16; cell += 256) {
-                const uint32_t bits = (uint32_t)(there >> (cell / D * 8)) & 0xffu;
-                u32x4 w = *reinterpret_cast<const u32x4 *>(vb + cell * 16);
-                if (bits != 0xffu) {
+    };
+    auto largest = [&](const Scores &s) {
+        float top = minus_inf();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] &= (bits >> (2 * i) & 1 ? 0xffffu : 0u) | (bits >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-                    *reinterpret_cast<u32x4 *>(vb + cell * 16) = w;
-                }
-                bad = bad || not_finite(w);
-            }
-            by_hand = __syncthreads_or(bad);
-        }
-        const bool active = wave_live && k0 <= wave_max;
-        u32x4 p[NVS];
-        if (active) {
-            f32x16 s[NB];
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, s[b][j]);
+        return top;
+    };
+    // the running maximum and everything that is relative to it
+    auto raise = [&](float top) {
+        if (!__any(top > mx + slack)) return;
+        const float now = fmaxf(mx, fmaxf(top, __shfl_xor(top, 32, 64)));
+        const float f = now == minus_inf() ? 1.0f : __builtin_amdgcn_exp2f((mx - now) * cs);
+        mx = now;
+        mc = now == minus_inf() ? 0.0f : now * cs;
+        l *= f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[b][j] = 0.0f;
+        for (int i = 0; i < ND; ++i) o[i] *= f;
+    };
+    typedef u32x4 Weights[NVS];
+    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+    // two of the lane's scores as weights: pair y of 8 NB
+    auto weigh = [&](const Scores &s, Weights &p, int y) {
+        const int b = y / 8, j = y % 8 * 2;
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], cs, -mc));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j + 1], cs, -mc));
+        uint32_t w = pk_bf16(p0, p1);
+        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, l, false);
+        asm volatile("" : "+v"(w), "+v"(l));  // here, beside the products, and not where it is used
+        p[2 * b + j / 8][j % 8 / 2] = w;
+    };
+    auto add = [&](const Weights &p, const bf16x8 &vf, int x) {
+        o[x % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8, p[x / ND]), o[x % ND], 0, 0, 0);
+    };
+    // A tile that some row does not read whole.  A weight of 0 does not keep
+    // an infinity or NaN in V out of the sum, so tokens that are not there
+    // become 0; returns whether a token that is there is not finite.
+    auto clean = [&](int kt, uint64_t there) -> bool {
+        uint8_t *vb = tile_lds + values_at(kt);
+        bool bad = false;
+        for (int cell = tid; cell < TB / 16; cell += 256) {
+            const uint32_t bits = (uint32_t)(there >> (cell / D * 8)) & 0xffu;
+            u32x4 w = *reinterpret_cast<const u32x4 *>(vb + cell * 16);
+            if (bits != 0xffu) {
 #pragma unroll
-                for (int j = 0; j < NKS; ++j) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(kb + ((2 * j + hf) * TK + 32 * b + krow) * 16);
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[b], 0, 0, 0);
-                }
-            }
-            if (there != ALL || k0 + TK - 1 > wave_min) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    // bit i: the token 8 hf + i of the block is there and not after the row
-                    const int last = pos - (k0 + 32 * b + 8 * hf);
-                    uint32_t ok = (uint32_t)(there >> (32 * b + 8 * hf));
-                    ok &= last < 0 ? 0u : last > 30 ? 0xffffffffu : (2u << last) - 1;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (!(ok >> (j / 8 * 16 + j % 8) & 1)) s[b][j] = minus_inf();
-                }
-            }
-            float top = minus_inf();
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) top = fmaxf(top, s[b][j]);
-            if (__any(top > mx + slack)) {
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float now = fmaxf(mx, top);
-                const float f = now == minus_inf() ? 1.0f : __builtin_amdgcn_exp2f((mx - now) * cs);
-                mx = now;
-                mc = now == minus_inf() ? 0.0f : now * cs;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < ND; ++i) o[i] *= f;
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], cs, -mc));
-                    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j + 1], cs, -mc));
-                    l += p0;
-                    l += p1;
-                    p[2 * b + j / 8][j % 8 / 2] = pk_bf16(p0, p1);
-                }
-        }
-        if (by_hand) {
-            if (active)
-                for (int t = 0; t < TK; ++t) {
-                    if (!(there >> t & 1)) continue;
-#pragma unroll
-                    for (int i = 0; i < ND; ++i)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int d = 32 * i + 8 * (j / 4) + 4 * hf + j % 4;
-                            const uint32_t w = *reinterpret_cast<const uint16_t *>(vb + (t / 8 * D + d) * 16 + t % 8 * 2);
-                            if ((w & 0x7f80u) == 0x7f80u && k0 + t <= pos) o[i][j] += bf16_lo(w);
-                        }
-                }
-            __syncthreads();
-            for (int cell = tid; cell < TB / 16; cell += 256) {
-                u32x4 w = *reinterpret_cast<const u32x4 *>(vb + cell * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-                    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
-                }
+                for (int i = 0; i < 4; ++i)
+                    w[i] &= (bits >> (2 * i) & 1 ? 0xffffu : 0u) | (bits >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
                 *reinterpret_cast<u32x4 *>(vb + cell * 16) = w;
             }
-            __syncthreads();
+            bad = bad || not_finite(w);
         }
-        if (active) {
+        return __syncthreads_or(bad);
+    };
+    // ... whose column is then added to the rows that read it by hand, and becomes 0 for the product.
+    auto by_hand = [&](int kt, uint64_t there, bool active) {
+        uint8_t *vb = tile_lds + values_at(kt);
+        if (active)
+            for (int t = 0; t < TK; ++t) {
+                if (!(there >> t & 1)) continue;
 #pragma unroll
-            for (int j = 0; j < NVS; ++j)
+                for (int i = 0; i < ND; ++i)
 #pragma unroll
-                for (int i = 0; i < ND; ++i) {
-                    const bf16x8 vf = *reinterpret_cast<const bf16x8 *>(vb + ((2 * j + hf) * D + 32 * i + m) * 16);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8, p[j]), o[i], 0, 0, 0);
-                }
+                    for (int j = 0; j < 16; ++j) {
+                        const int d = 32 * i + 8 * (j / 4) + 4 * hf + j % 4;
+                        const uint32_t w = *reinterpret_cast<const uint16_t *>(vb + (t / 8 * D + d) * 16 + t % 8 * 2);
+                        const float v = (w & 0x7f80u) == 0x7f80u ? bf16_lo(w) : 0.0f;
+                        o[i][j] += kt * TK + t <= pos ? v : 0.0f;
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+        __syncthreads();
+        for (int cell = tid; cell < TB / 16; cell += 256) {
+            u32x4 w = *reinterpret_cast<const u32x4 *>(vb + cell * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+            }
+            *reinterpret_cast<u32x4 *>(vb + cell * 16) = w;
         }
-        if (E4M3 && more) widen(buf ^ 1);
-        there = there_next;
+        __syncthreads();
+    };
+    auto active = [&](int kt) { return wave_live && kt < t1 && kt * TK <= wave_max; };
+
+    // the pages and the tokens that are there of tile t (there0), t + 1 (e1, there1) and t + 2 (e2)
+    int e1 = entry(t0), e2;
+    uint64_t there0 = __ballot(e1 >= 0) & ALL, there1;
+    Scores sa, sb;
+    if (t0 < t1) {
+        const int e0 = e1;
+        e1 = entry(t0 + 1);
+        e2 = entry(t0 + 2);
+        there1 = __ballot(e1 >= 0) & ALL;
+        if (E4M3) {
+            load_keys(t0, e0);
+            load_values(t0, e0);
+#pragma unroll
+            for (int y = 0; y < PIECES; ++y) widen(t0, t0, y);
+            load_keys(t0 + 1, e1);
+            lds::barrier_no_fence();
+        } else {
+            const uint8_t *k0 = keys_from(t0, e0), *k1 = keys_from(t0 + 1, e1), *v0[GROUPS];
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) v0[i] = values_from(t0, e0, i);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) fetch_keys(t0, k0, i);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) fetch_keys(t0 + 1, k1, i);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) fetch_values(t0, v0, i);
+            lds::wait_vm<2 * NI>();
+            lds::barrier_no_fence();
+        }
+        if (active(t0)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) zero(sa, b);
+#pragma unroll
+            for (int x = 0; x < NK; ++x) score(sa, key_frag(t0, x), x);
+            mask(sa, t0, there0);
+            raise(largest(sa));
+        }
+        if (E4M3) {
+#pragma unroll
+            for (int y = 0; y < PIECES; ++y)
+                if (y % 6 < 2) widen(t0 + 1, 0, y);
+            load_keys(t0 + 2, e2);
+            load_values(t0 + 1, e1);
+        }
     }
+    // Tile kt, whose scores are in s; the next one's come into n.  The source
+    // is laid out as it runs (sched_barrier): an operand is read four products
+    // ahead, and the fetches of the tiles to come and the weights stand
+    // between the products, of which each takes as long as eight vector
+    // instructions.
+    auto step = [&](Scores &s, Scores &n, int kt) {
+        constexpr int AHEAD = 4, PAIRS = 8 * NB, EARLY = PAIRS * 5 / 8;  // pairs weighed beside the scores' products
+        if (!E4M3) lds::wait_vm<0>();
+        lds::barrier_no_fence();  // tile kt's values and the next one's keys are in, and no wave reads those before any more
+        const uint8_t *kp = nullptr, *vp[GROUPS];
+        if (!E4M3) {
+            kp = keys_from(kt + 2, e2);
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) vp[i] = values_from(kt + 1, e1, i);
+        }
+        e1 = e2;
+        e2 = entry(kt + 3);
+        const bool now = active(kt), next = active(kt + 1);
+        if ((there0 != ALL || kt * TK + TK - 1 > tile_min) && clean(kt, there0)) by_hand(kt, there0, now);
+        Weights p;
+        bf16x8 f[AHEAD];
+        __builtin_amdgcn_s_setprio(1);  // before waves that fetch
+        if (next) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) f[x] = key_frag(kt + 1, x);
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (x % NKS == 0) zero(n, x / NKS);
+                score(n, f[x % AHEAD], x);
+                f[x % AHEAD] = x + AHEAD < NK ? key_frag(kt + 1, x + AHEAD) : value_frag(kt, x + AHEAD - NK);
+                if (!E4M3)
+#pragma unroll
+                    for (int i = x * 2 * NI / NK; i < (x + 1) * 2 * NI / NK; ++i) {
+                        if (i < NI) fetch_keys(kt + 2, kp, i);
+                        else fetch_values(kt + 1, vp, i - NI);
+                    }
+#pragma unroll
+                for (int y = x * EARLY / NK; y < (x + 1) * EARLY / NK; ++y) weigh(s, p, y);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            mask(n, kt + 1, there1);
+        } else {
+            if (!E4M3) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) fetch_keys(kt + 2, kp, i);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) fetch_values(kt + 1, vp, i);
+            }
+            if (now) {
+#pragma unroll
+                for (int y = 0; y < EARLY; ++y) weigh(s, p, y);
+#pragma unroll
+                for (int x = 0; x < AHEAD; ++x) f[x] = value_frag(kt, x);
+            }
+        }
+        if (now) {
+            float top = minus_inf();
+#pragma unroll
+            for (int x = 0; x < NV; ++x) {
+                __builtin_amdgcn_sched_barrier(0);
+                add(p, f[x % AHEAD], x);
+                if (x + AHEAD < NV) f[x % AHEAD] = value_frag(kt, x + AHEAD);
+                // the last pairs, before the product that needs the first of them
+#pragma unroll
+                for (int y = EARLY + x * 2 * (PAIRS - EARLY) / NV; y < EARLY + (x + 1) * 2 * (PAIRS - EARLY) / NV && y < PAIRS; ++y)
+                    weigh(s, p, y);
+                if (BETWEEN)
+#pragma unroll
+                    for (int y = x * PIECES / NV; y < (x + 1) * PIECES / NV; ++y) widen(kt + 2, kt + 1, y);
+                if (x == NV - NV / 4) top = largest(n);  // (of no use if there is no next tile)
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (next) raise(top);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        if (E4M3) {
+            if (!now || !BETWEEN)
+#pragma unroll
+                for (int y = 0; y < PIECES; ++y) widen(kt + 2, kt + 1, y);
+            load_keys(kt + 3, e2);
+            load_values(kt + 2, e1);
+        }
+        there0 = there1;
+        there1 = __ballot(e1 >= 0) & ALL;
+    };
+    for (int kt = t0; kt < t1; kt += 2) {
+        step(sa, sb, kt);
+        if (kt + 1 < t1) step(sb, sa, kt + 1);
+    }
+    lds::wait_vm<0>();  // the last fetches (of no tile) may not outlive the workgroup's LDS
     if (!live) return;
     l += __shfl_xor(l, 32, 64);
     if (u.split == 1) {
+        const size_t at = (size_t)(u.first + token) * a.ldo + (size_t)(h * G + x % G) * D;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int i = 0; i < ND; ++i)
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<uint2 *>(a.out + out_at + 32 * i + 2 * j + 4 * hf) =
+                *reinterpret_cast<uint2 *>(a.out + at + 32 * i + 2 * j + 4 * hf) =
                     make_uint2(pk_bf16(o[i][j] * inv, o[i][j + 1] * inv), pk_bf16(o[i][j + 2] * inv, o[i][j + 3] * inv));
     } else {
         const size_t at = ((size_t)u.slot * H + h) * a.part_rows + wave * 32 + m;
@@ -695,6 +843,7 @@ __global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
     typedef float vec __attribute__((ext_vector_type(V)));
     const int lane = threadIdx.x & 63, H = a.c.heads, G = a.heads_q / H;
     const int QT = PREFILL ? 1 : (G + kDecodeRows - 1) / kDecodeRows, HT = H * QT;
+    if (a.info[a.n].x == 0) return;
     const int rows = PREFILL ? min(max(a.starts[a.n], 0), a.t) : a.n;
     for (int item = blockIdx.x * 4 + (threadIdx.x >> 6); item < rows * a.heads_q; item += gridDim.x * 4) {
         const int r = item / a.heads_q, hq = item % a.heads_q, h = hq / G;
@@ -756,10 +905,13 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
     const int tiles = prefill ? a.t * G / kPrefillRows + a.n : a.n;
     const dim3 grid((unsigned)(((prefill ? kPrefillTarget : kDecodeTarget) / HT + tiles) * HT)), block(256);
     const bool few = a.n <= 64;
-    if (prefill && few) hipLaunchKernelGGL((k_prefill<CT, D, true>), grid, block, 0, s, a);
-    else if (prefill) hipLaunchKernelGGL((k_prefill<CT, D, false>), grid, block, 0, s, a);
-    else if (few) hipLaunchKernelGGL((k_decode<CT, D, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_decode<CT, D, false>), grid, block, 0, s, a);
+    if (prefill) {
+        if (few) hipLaunchKernelGGL((k_prefill<CT, D, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_prefill<CT, D, false>), grid, block, 0, s, a);
+    } else {
+        if (few) hipLaunchKernelGGL((k_decode<CT, D, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_decode<CT, D, false>), grid, block, 0, s, a);
+    }
     if (hipError_t e = hipGetLastError()) return e;
     if (a.max_tokens <= (prefill ? kPrefillLeast : kDecodeLeast)) return hipSuccess;  // nothing is cut
     const int64_t items = (int64_t)(prefill ? a.t : a.n) * a.heads_q;
@@ -779,9 +931,10 @@ hipError_t launch_head(const AttentionArgs &a, hipStream_t s) {
 }  // namespace
 
 AttentionPlan attention_plan(bool prefill, int t, int n, int heads_q, int heads, int head) {
-    const int G = heads_q / heads, tile = prefill ? kPrefillRows : kDecodeRows;
+    const int G = heads_q / heads;
+    const int tile = prefill ? kPrefillRows : kDecodeRows;
     const int HT = prefill ? heads : heads * ((G + kDecodeRows - 1) / kDecodeRows);
-    const int target = (prefill ? kPrefillTarget : kDecodeTarget) / HT, tiles = prefill ? t * G / kPrefillRows + n : n;
+    const int target = (prefill ? kPrefillTarget : kDecodeTarget) / HT, tiles = prefill ? t * G / tile + n : n;
     AttentionPlan p;
     const int64_t pairs = prefill ? (int64_t)t * G : G;
     p.part_rows = prefill ? (int)(pairs < tile ? (pairs + 31) / 32 * 32 : tile) : (G < tile ? G : tile);
@@ -791,7 +944,7 @@ AttentionPlan attention_plan(bool prefill, int t, int n, int heads_q, int heads,
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t rows = (size_t)p.slots * HT * p.part_rows;
     p.info = 0;
-    p.stats = up((size_t)n * sizeof(int2));
+    p.stats = up(((size_t)n + 1) * sizeof(int2));
     p.part = p.stats + up(rows * sizeof(float2));
     p.total = p.part + up(rows * head * sizeof(float));
     return p;

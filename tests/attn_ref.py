@@ -93,8 +93,10 @@ def attention(q, k, v, positions, scale, weight_half):
     magnitudes, and the weight's exponent adds the roundings of scale * log2 e, of the product and of the largest
     score's (each half a step of at most the largest |score|) and two of exp2's result: delta in all, relative to the
     weight.  The weights' and the outputs' sums over n tokens are fp32: at most n + 64 steps (parts and their joining
-    included) of half a step of their magnitude, twice that in the matrix core.  Weights meet v rounded by at most
-    weight_half of their value (relative)."""
+    included) of half a step of their magnitude, twice that in the matrix core.  Weights are rounded by factors
+    1 + e_j, |e_j| <= weight_half, before they are summed and meet v, which moves the output w.v to
+    sum w_j (1 + e_j) v_j / sum w_j (1 + e_j) = w.v + sum w_j e_j (v_j - w.v) / (1 + sum w_j e_j): by at most
+    weight_half (sum w_j |v_j| + |w.v|) (1 + 2 weight_half)."""
     rows, hq, d = q.shape
     n, hk, _ = k.shape
     g = hq // hk
@@ -117,8 +119,10 @@ def attention(q, k, v, positions, scale, weight_half):
         big = torch.where(seen, mag, 0.0).amax(1, keepdim=True)
         delta = (2 * d + 8) * U32 * big + 8 * U32 + 2 * (n + 64) * U32
         vw = w @ vh.abs()
-        err[:, h] = 2 * delta * vw * 1.01 + weight_half * vw
-        var[:, h] = (weight_half ** 2) * (w ** 2 @ vh ** 2)
+        o = out[:, h]
+        err[:, h] = 2 * delta * vw * 1.01 + weight_half * (1 + 2 * weight_half) * (vw + o.abs())
+        w2 = w ** 2
+        var[:, h] = (weight_half ** 2) * (w2 @ vh ** 2 - 2 * o * (w2 @ vh) + o ** 2 * w2.sum(1, keepdim=True)).clamp_min(0)
     return out, err, var
 
 
