@@ -34,9 +34,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.0f;  // log2 of the largest weight
 
-// About how many units the tiles are cut into, and the fewest tokens of one.
-constexpr int kDecodeTarget = 2048, kDecodeLeast = 128;
-constexpr int kPrefillTarget = 512, kPrefillLeast = 256;
+// How many tokens a part has: as many as make `few` units of all tiles, but
+// from `least` to `enough`; and at least as many as make `many` units.  The
+// chip holds 512 workgroups at a time (256 of heads of 256).  Decode: with
+// {512, 128, 1024, 2048} one sequence of 1000 tokens takes 8.4 us and one of
+// 32000 35 us (2048 units of 128 and more: 10.3 and 45), 32 of 16000 359 (1024:
+// 363).  Prefill: more than 512 units were slower wherever tiles were cut.  A
+// full tile's part costs 66 KB written and read again, so such tiles have parts
+// of twice `least` (512 rows of one sequence 23.4 -> 18.8 us); tiles of few
+// rows gain from shorter ones (64 rows after 4 x 2000 tokens 18.9 -> 15.9).
+struct Cut {
+    int few, least, enough, many;
+};
+constexpr Cut kDecodeCut = {512, 128, 1024, 2048}, kPrefillCut = {256, 256, 1024, 512};
 
 __device__ __forceinline__ float minus_inf() { return -__builtin_inff(); }
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
@@ -70,6 +80,7 @@ struct Unit {
 // One sequence as the units see it.
 struct Seq {
     int len, rows, first, tiles;
+    int least;  // tokens of a part at the least
 };
 template <bool PREFILL>
 __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) {
@@ -77,22 +88,29 @@ __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) 
     q.len = min(max(a.length[s], 0), a.max_tokens);
     q.first = s;
     q.rows = q.tiles = 1;
+    q.least = PREFILL ? kPrefillCut.least : kDecodeCut.least;
     if (PREFILL || a.starts) {
         const int end = min(max(a.starts[s + 1], 0), a.t);
         q.first = min(max(a.starts[s], 0), a.t);
         q.rows = max(end - q.first, 0);
         q.tiles = PREFILL ? (q.rows * group + kPrefillRows - 1) / kPrefillRows : min(q.rows, 1);
         if (!PREFILL) q.first = end - 1;
+        if (PREFILL && q.tiles > 1) q.least *= 2;
     }
     return q;
 }
 // Tokens that a part has, for tiles of `work` tokens in all and heads (head tiles) of them.
 template <bool PREFILL>
 __device__ __forceinline__ int part_tokens(int64_t work, int heads) {
-    constexpr int TARGET = PREFILL ? kPrefillTarget : kDecodeTarget, LEAST = PREFILL ? kPrefillLeast : kDecodeLeast;
-    return (int)min(max((work * heads + TARGET - 1) / TARGET, (int64_t)LEAST), (int64_t)1 << 30);
+    constexpr Cut cut = PREFILL ? kPrefillCut : kDecodeCut;
+    work *= heads;
+    const int64_t few = min(max((work + cut.few - 1) / cut.few, (int64_t)cut.least), (int64_t)cut.enough);
+    return (int)min(max((work + cut.many - 1) / cut.many, few), (int64_t)1 << 30);
 }
-__device__ __forceinline__ int splits(const Seq &q, int tokens) { return max((q.len + tokens - 1) / tokens, 1); }
+__device__ __forceinline__ int splits(const Seq &q, int tokens) {
+    tokens = max(tokens, q.least);
+    return max((q.len + tokens - 1) / tokens, 1);
+}
 
 template <class T>
 __device__ __forceinline__ T wave_scan(T v) {  // inclusive
@@ -112,7 +130,7 @@ template <bool PREFILL, bool SMALL>
 __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int group, int heads, Unit &u) {
     const int tid = threadIdx.x, lane = tid & 63;
     if (SMALL) {
-        Seq q = {0, 0, 0, 0};
+        Seq q = {0, 0, 0, 0, 1};
         if (lane < a.n) q = seq_of<PREFILL>(a, lane, group);
         int64_t work = (int64_t)q.tiles * q.len;
 #pragma unroll
@@ -203,7 +221,7 @@ __device__ __forceinline__ void leave_info(const AttentionArgs &a, const Unit &u
 // second product as two bf16 terms, p = hi + lo, which costs nothing where
 // memory is the bound.  Bound by memory.
 template <int CT, int D, bool SMALL>
-__global__ void __launch_bounds__(256) k_decode(AttentionArgs a) {
+__global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16 ? 2 : 1) k_decode(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;
     constexpr int SIZE = E4M3 ? 1 : 2, TK = E4M3 ? 64 : 32, NB = TK / 16, KEYS = TK / 4;  // KEYS: of one lane
     constexpr int KL = E4M3 ? D / 64 : D / 32, VL = D / 16;                               // loads a block of 16, a tile
@@ -212,11 +230,11 @@ __global__ void __launch_bounds__(256) k_decode(AttentionArgs a) {
     const KvCache &c = a.c;
     const int G = a.heads_q / c.heads, QT = (G + 15) / 16, HT = c.heads * QT;
     const int ht = blockIdx.x % HT, h = ht / QT, q0 = ht % QT * 16, nq = min(16, G - q0);
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Unit u;
     if (!find_unit<false, SMALL>(a, blockIdx.x / HT, G, HT, u)) return;
     leave_info(a, u, ht);
-    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // parts of equal numbers of tiles
     const int tiles = (u.len + TK - 1) / TK, each = (tiles + u.split - 1) / u.split;
     const int t0 = u.part * each, t1 = min(t0 + each, tiles);
@@ -835,64 +853,110 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
 
 // ------------------------------------------------------------------ joining
 
-// A wave a (row, query head) whose tile several workgroups shared: the partial
-// outputs weighted by 2^(m - largest m), over the sum of the weights, in order.
-template <bool PREFILL, int D>
+// Where the parts of a (row, query head) stand: slots slot0 .. slot0 + split - 1
+// at row `in` of head tile ht; false if it was not cut, or is no sequence's.
+struct Parts {
+    int split, slot0, ht, in, to;
+};
+template <bool PREFILL>
+__device__ __forceinline__ bool parts_of(const AttentionArgs &a, int r, int hq, int G, int QT, Parts &p) {
+    int s = r, tile = 0;
+    p.to = r;
+    if (PREFILL) {
+        int lo = 0, hi = a.n;  // the last sequence whose first row is at most r
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.starts[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        s = lo;
+        const Seq q = seq_of<true>(a, s, G);
+        if (r < q.first || r >= q.first + q.rows) return false;
+        const int x = (r - q.first) * G + hq % G;
+        tile = x / kPrefillRows;
+        p.in = x % kPrefillRows;
+        p.ht = hq / G;
+    } else {
+        const Seq q = seq_of<false>(a, s, G);
+        if (!q.tiles) return false;
+        p.to = q.first;
+        p.ht = hq / G * QT + hq % G / kDecodeRows;
+        p.in = hq % G % kDecodeRows;
+    }
+    const int2 info = a.info[s];
+    p.split = info.x;
+    p.slot0 = info.y + tile * p.split;
+    return p.split >= 2 && p.slot0 >= 0 && p.slot0 <= a.slots - p.split;
+}
+
+// The parts of rows whose tiles were cut: outputs weighted by 2^(m - largest
+// m), over the sum of the weights, in order.  A wave a (row, query head), or
+// where those are few and may have hundreds of parts (WIDE) a workgroup, whose
+// waves take runs of them: 1 row x 32 heads of 32 parts, prefill, 23.1 -> 16.2 us.
+// Bound by the parts' bytes, or by latency.
+template <bool PREFILL, int D, bool WIDE>
 __global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
     constexpr int V = D / 64;  // columns a lane
     typedef float vec __attribute__((ext_vector_type(V)));
-    const int lane = threadIdx.x & 63, H = a.c.heads, G = a.heads_q / H;
+    __shared__ vec wave_sum[WIDE ? 3 : 1][64];
+    __shared__ float wave_l[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, H = a.c.heads, G = a.heads_q / H;
     const int QT = PREFILL ? 1 : (G + kDecodeRows - 1) / kDecodeRows, HT = H * QT;
     if (a.info[a.n].x == 0) return;
     const int rows = PREFILL ? min(max(a.starts[a.n], 0), a.t) : a.n;
-    for (int item = blockIdx.x * 4 + (threadIdx.x >> 6); item < rows * a.heads_q; item += gridDim.x * 4) {
-        const int r = item / a.heads_q, hq = item % a.heads_q, h = hq / G;
-        int s = r, to = r, tile = 0, ht, in;
-        if (PREFILL) {
-            int lo = 0, hi = a.n;  // the last sequence whose first row is at most r
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (a.starts[mid] <= r) lo = mid;
-                else hi = mid;
-            }
-            s = lo;
-            const Seq q = seq_of<true>(a, s, G);
-            if (r < q.first || r >= q.first + q.rows) continue;
-            const int x = (r - q.first) * G + hq % G;
-            tile = x / kPrefillRows;
-            in = x % kPrefillRows;
-            ht = h;
-        } else {
-            const Seq q = seq_of<false>(a, s, G);
-            if (!q.tiles) continue;
-            to = q.first;
-            ht = h * QT + hq % G / kDecodeRows;
-            in = hq % G % kDecodeRows;
-        }
-        const int2 info = a.info[s];
-        const int split = info.x, slot0 = info.y + tile * split;
-        if (split < 2 || slot0 < 0 || slot0 > a.slots - split) continue;
-        auto place = [&](int i) { return ((size_t)(slot0 + i) * HT + ht) * a.part_rows + in; };
-        float top = minus_inf();
-        for (int i = lane; i < split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
+    const int step = WIDE ? gridDim.x : gridDim.x * 4;
+    for (int item = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave; item < rows * a.heads_q; item += step) {
+        const int hq = item % a.heads_q;
+        Parts p;
+        if (!parts_of<PREFILL>(a, item / a.heads_q, hq, G, QT, p)) continue;  // (WIDE: for all four waves)
+        auto place = [&](int i) { return ((size_t)(p.slot0 + i) * HT + p.ht) * a.part_rows + p.in; };
+        const int each = (p.split + 3) / 4, i0 = WIDE ? wave * each : 0, i1 = WIDE ? min(i0 + each, p.split) : p.split;
+        // the first parts are asked for before the maximum is known
+        constexpr int FIRST = WIDE ? 8 : 4;
+        vec part[FIRST];
+#pragma unroll
+        for (int i = 0; i < FIRST; ++i)
+            if (i0 + i < i1) part[i] = *reinterpret_cast<const vec *>(a.part + place(i0 + i) * D + lane * V);
+        float2 mine = make_float2(minus_inf(), 0.0f);  // part `lane` of the first 64
+        if (lane < p.split) mine = a.stats[place(lane)];
+        float top = mine.x;
+        for (int i = lane + 64; i < p.split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
         vec sum;
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] = 0.0f;
         float l = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < split; ++i) {
-            const float2 st = a.stats[place(i)];
+        auto add = [&](int i, vec v) {
+            const float2 st = i < 64 ? make_float2(__shfl(mine.x, i, 64), __shfl(mine.y, i, 64)) : a.stats[place(i)];
             const float f = st.x == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
             l += f * st.y;
-            sum += f * *reinterpret_cast<const vec *>(a.part + place(i) * D + lane * V);
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        __bf16 y[V];
+            sum += f * v;
+        };
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = (__bf16)(sum[j] * inv);
-        __builtin_memcpy(__builtin_assume_aligned(a.out + to * a.ldo + (size_t)hq * D + lane * V, 2 * V), y, 2 * V);
+        for (int i = 0; i < FIRST; ++i)
+            if (i0 + i < i1) add(i0 + i, part[i]);
+        for (int i = i0 + FIRST; i < i1; ++i) add(i, *reinterpret_cast<const vec *>(a.part + place(i) * D + lane * V));
+        if (WIDE) {
+            if (wave > 0) wave_sum[WIDE ? wave - 1 : 0][lane] = sum;
+            if (lane == 0) wave_l[wave] = l;
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < 4; ++w) {
+                    sum += wave_sum[WIDE ? w - 1 : 0][lane];
+                    l += wave_l[w];
+                }
+            }
+        }
+        if (!WIDE || wave == 0) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            __bf16 y[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[j] = (__bf16)(sum[j] * inv);
+            __builtin_memcpy(__builtin_assume_aligned(a.out + p.to * a.ldo + (size_t)hq * D + lane * V, 2 * V), y, 2 * V);
+        }
+        if (WIDE) __syncthreads();
     }
 }
 
@@ -903,7 +967,11 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
     const int HT = prefill ? a.c.heads : a.c.heads * ((G + kDecodeRows - 1) / kDecodeRows);
     // no more units than this: the cuts that the target allows, and a unit a tile
     const int tiles = prefill ? a.t * G / kPrefillRows + a.n : a.n;
-    const dim3 grid((unsigned)(((prefill ? kPrefillTarget : kDecodeTarget) / HT + tiles) * HT)), block(256);
+    const Cut cut = prefill ? kPrefillCut : kDecodeCut;
+    // no more units of a head than the cuts make, and a unit a tile; nor than the tables' tokens allow
+    const int64_t most = (int64_t)tiles * ((a.max_tokens + cut.least - 1) / cut.least);
+    const int units = (int)(most < cut.many / HT + tiles ? most : cut.many / HT + tiles);
+    const dim3 grid((unsigned)(units * HT)), block(256);
     const bool few = a.n <= 64;
     if (prefill) {
         if (few) hipLaunchKernelGGL((k_prefill<CT, D, true>), grid, block, 0, s, a);
@@ -913,11 +981,16 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
         else hipLaunchKernelGGL((k_decode<CT, D, false>), grid, block, 0, s, a);
     }
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.max_tokens <= (prefill ? kPrefillLeast : kDecodeLeast)) return hipSuccess;  // nothing is cut
+    if (a.max_tokens <= cut.least) return hipSuccess;  // nothing is cut
+    // 2048 workgroups fill the chip; more items are taken in turn
     const int64_t items = (int64_t)(prefill ? a.t : a.n) * a.heads_q;
-    const dim3 join((unsigned)((items < 8192 ? items : 8192) + 3) / 4);
-    if (prefill) hipLaunchKernelGGL((k_join<true, D>), join, block, 0, s, a);
-    else hipLaunchKernelGGL((k_join<false, D>), join, block, 0, s, a);
+    const bool wide = items <= 4096;
+    const int64_t blocks = wide ? items : (items + 3) / 4;
+    const dim3 join((unsigned)(blocks < 2048 ? blocks : 2048));
+    if (prefill && wide) hipLaunchKernelGGL((k_join<true, D, true>), join, block, 0, s, a);
+    else if (prefill) hipLaunchKernelGGL((k_join<true, D, false>), join, block, 0, s, a);
+    else if (wide) hipLaunchKernelGGL((k_join<false, D, true>), join, block, 0, s, a);
+    else hipLaunchKernelGGL((k_join<false, D, false>), join, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -934,7 +1007,7 @@ AttentionPlan attention_plan(bool prefill, int t, int n, int heads_q, int heads,
     const int G = heads_q / heads;
     const int tile = prefill ? kPrefillRows : kDecodeRows;
     const int HT = prefill ? heads : heads * ((G + kDecodeRows - 1) / kDecodeRows);
-    const int target = (prefill ? kPrefillTarget : kDecodeTarget) / HT, tiles = prefill ? t * G / tile + n : n;
+    const int target = (prefill ? kPrefillCut : kDecodeCut).many / HT, tiles = prefill ? t * G / tile + n : n;
     AttentionPlan p;
     const int64_t pairs = prefill ? (int64_t)t * G : G;
     p.part_rows = prefill ? (int)(pairs < tile ? (pairs + 31) / 32 * 32 : tile) : (G < tile ? G : tile);
