@@ -19,6 +19,7 @@
 
 #include "attn.h"
 #include "lds_dma.h"
+#include "wave_scan.h"
 
 namespace moe {
 namespace {
@@ -101,26 +102,16 @@ __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) 
 }
 // Tokens that a part has, for tiles of `work` tokens in all and heads (head tiles) of them.
 template <bool PREFILL>
-__device__ __forceinline__ int part_tokens(int64_t work, int heads) {
+__device__ __forceinline__ int part_tokens(float work, int heads) {
     constexpr Cut cut = PREFILL ? kPrefillCut : kDecodeCut;
+    // (fp32 is off by 2^-20 of it at most, by which no count of units can pass the next whole number)
     work *= heads;
-    const int64_t few = min(max((work + cut.few - 1) / cut.few, (int64_t)cut.least), (int64_t)cut.enough);
-    return (int)min(max((work + cut.many - 1) / cut.many, few), (int64_t)1 << 30);
+    const float few = fminf(fmaxf(work / cut.few, (float)cut.least), (float)cut.enough);
+    return (int)fminf(ceilf(fmaxf(work / cut.many, few)), 1073741824.0f);
 }
 __device__ __forceinline__ int splits(const Seq &q, int tokens) {
     tokens = max(tokens, q.least);
     return max((q.len + tokens - 1) / tokens, 1);
-}
-
-template <class T>
-__device__ __forceinline__ T wave_scan(T v) {  // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const T o = __shfl_up(v, off, 64);
-        if (lane >= off) v += o;
-    }
-    return v;
 }
 
 // Unit v of a head: lengths are known on the GPU only, so each workgroup finds
@@ -132,9 +123,7 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
     if (SMALL) {
         Seq q = {0, 0, 0, 0, 1};
         if (lane < a.n) q = seq_of<PREFILL>(a, lane, group);
-        int64_t work = (int64_t)q.tiles * q.len;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) work += __shfl_xor(work, off, 64);
+        const float work = wave_sum((float)q.tiles * q.len);
         const int n = lane < a.n ? splits(q, part_tokens<PREFILL>(work, heads)) : 0;
         const int units = q.tiles * n, parts = n > 1 ? units : 0;
         const int ue = wave_scan(units), pe = wave_scan(parts);
@@ -146,17 +135,16 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
         u = Unit{s, get(q.len), get(q.rows), get(q.first), tiles - 1 - at / n_s, n_s, at % n_s, get(pe - parts),
                  __builtin_amdgcn_readlane(pe, 63)};
     } else {
-        __shared__ int64_t wave_work[4];
+        __shared__ float wave_work[4];
         __shared__ int wave_units[4], wave_parts[4];
         __shared__ Unit found;
         const int per = (a.n + 255) / 256, s0 = tid * per, s1 = min(s0 + per, a.n), wave = tid >> 6;
-        int64_t work = 0;
+        float work = 0.0f;
         for (int s = s0; s < s1; ++s) {
             const Seq q = seq_of<PREFILL>(a, s, group);
-            work += (int64_t)q.tiles * q.len;
+            work += (float)q.tiles * q.len;
         }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) work += __shfl_xor(work, off, 64);
+        work = wave_sum(work);
         if (lane == 0) wave_work[wave] = work;
         if (tid == 0) found.s = -1;
         __syncthreads();
