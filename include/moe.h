@@ -725,14 +725,15 @@ size_t moe_attention_workspace_bytes(int32_t t, int32_t n, int32_t heads_q, cons
  * where query head h reads key head h / (heads_q / heads).  Token j is in
  * page table[s][j / page].  A length outside 0 .. max_pages * page counts as
  * the nearest of these, and tokens of pages that the cache lacks (entries
- * outside 0 .. pages - 1) as not there.  A row without any token is 0.
+ * outside 0 .. pages - 1) as not there.  A row without any token is 0, and
+ * so is one all of whose scores are minus infinity.
  * Tokens that are not there, whatever their bytes hold, reach no output.
  *
  *   q      bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
  *   starts NULL: row s is sequence s's, t = n.  Else [n + 1], ascending, 0 .. t: the row of
  *          sequence s is the last of starts[s] .. starts[s + 1] - 1; sequences without
  *          rows are passed over, other rows left as they are
- *   table  [n][max_pages], row stride ldt;  length [n];  scale > 0, finite
+ *   table  [n][max_pages], row stride ldt;  length [n];  scale at least 2^-126, finite
  * Rows 16-byte aligned, at most 2^22 elements apart; out must not overlap
  * anything else.  Requires 1 <= t, n <= MOE_MAX_ROWS, heads_q a multiple of
  * heads up to 1024, max_pages * page <= 2^30; MOE_ERR_WORKSPACE for a

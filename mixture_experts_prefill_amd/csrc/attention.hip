@@ -33,7 +33,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kSlack = 8.0f;  // log2 of the largest weight
+constexpr float kSlack = 8.0f;         // log2 of the largest weight
+constexpr float kMostSlack = 1e38f;    // finite, so that the first score sets the maximum whatever the scale
 
 // How many tokens a part has: as many as make `few` units of all tiles, but
 // from `least` to `enough`; and at least as many as make `many` units.  The
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
             qf[j] = __builtin_bit_cast(bf16x8, w);
         }
     }
-    const float cs = a.scale * kLog2e, slack = kSlack / cs;
+    const float cs = a.scale * kLog2e, slack = fminf(kSlack / cs, kMostSlack);
     float mx = minus_inf(), mc = 0.0f, l = 0.0f;
     f32x4 o[VL];
 #pragma unroll
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
             qf[j] = __builtin_bit_cast(bf16x8, w);
         }
     }
-    const float cs = a.scale * kLog2e, slack = kSlack / cs;
+    const float cs = a.scale * kLog2e, slack = fminf(kSlack / cs, kMostSlack);
     float mx = minus_inf(), mc = 0.0f, l = 0.0f;
     f32x16 o[ND];
 #pragma unroll

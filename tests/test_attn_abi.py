@@ -170,7 +170,7 @@ ATTENTION_BAD = [(dict(t=0), CAPACITY), (dict(t=4097), CAPACITY), (dict(n=0), CA
                  (dict(table=None), INVALID), (dict(length=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
                  (dict(hq=0), INVALID), (dict(hq=5), INVALID), (dict(hq=-4), INVALID), (dict(hq=1026, ldq=70000, ldo=70000), INVALID),
                  (dict(max_pages=0), INVALID), (dict(max_pages=(1 << 25) + 1, ldt=1 << 26), INVALID), (dict(ldt=8), INVALID),
-                 (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+                 (dict(scale=0.0), INVALID), (dict(scale=1e-39), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
                  (dict(scale=float("inf")), INVALID), (dict(ldq=255), INVALID), (dict(ldq=260), INVALID), (dict(ldo=248), INVALID),
                  (dict(ldo=(1 << 22) + 8), INVALID), (dict(q=A + 8), INVALID), (dict(out=F + 4), INVALID),
                  (dict(cache=C + 8), INVALID), (dict(ws=G + 8), INVALID), (dict(table=D + 2), INVALID), (dict(length=E + 1), INVALID),

@@ -330,6 +330,35 @@ def test_sharp_and_flat_scores(mep, single, dtype):
             prefill(mep, b, [40], hq, kind, scale=1.0, q=q)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [2.0 ** -126, 1e-30, 1e-6, 1e3])
+def test_scales_of_any_size(mep, scale, dtype):
+    """Scales that make all weights equal, or one of them 1."""
+    b = Batch(mep, [300, 1, 700], 2, 64, 32, dtype)
+    decode(mep, b, 4, scale, scale=scale)
+    prefill(mep, b, [20, 1, 150], 4, scale, scale=scale)
+
+
+def test_scores_of_minus_infinity(mep):
+    """They weigh nothing; a row that has no other is 0."""
+    b = Batch(mep, [40, 40], 1, 64, 16, BF16)
+    x = torch.zeros(40, 1, 64)
+    x[:, 0, 0] = -torch.inf
+    b.cache.write("k", b.slots[0], x.to(BF16))
+    x[5, 0, 0] = 0.0
+    b.cache.write("k", b.slots[1], x.to(BF16))
+    q = torch.zeros(4, 64).to(BF16)
+    q[:, 0] = 1.0
+    cache, table, length = b.on_gpu()
+    out = torch.full((4, 64), GUARD, dtype=BF16, device="cuda")
+    ws = workspace(mep, 4, 2, 1, b.layout)
+    v = b.values(1)[1][5].view(-1).to(BF16).cuda()
+    mep.moe_attention_decode(q[:2].cuda(), b.layout, cache, table, length, 1.0, out[:2], ws)
+    assert bool((out[0] == 0).all()) and torch.equal(out[1], v)
+    mep.moe_attention_prefill(q.cuda(), ints([0, 2, 4]).cuda(), b.layout, cache, table, length, 1.0, out, ws)
+    assert bool((out[:2] == 0).all()) and torch.equal(out[2], v) and torch.equal(out[3], v)
+
+
 def test_equal_values_come_back(mep):
     """Weights that sum to 1: where every value is v, so is the output, to half a step."""
     n, head = 333, 128
