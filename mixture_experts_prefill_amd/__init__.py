@@ -596,19 +596,26 @@ def moe_kv_layout_make(pages: int, page: int, heads: int, head: int, dtype: torc
     return out
 
 
+_INT32 = torch.int32
+
+
 def _ints(x: torch.Tensor, n: int, dev: int, what: str) -> int:
     """The pointer of n contiguous int32 on GPU `dev`."""
-    if x.dtype != torch.int32:
+    # one test for the common case: the smallest calls take as long as their arguments
+    if x.dtype is _INT32 and x.get_device() == dev and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
+    if x.dtype != _INT32:
         raise ValueError(f"{what} must be int32, not {x.dtype}")
     return _flat(x, n, dev, what)
 
 
 def _table_args(table: torch.Tensor, n: int, dev: int):
     """(pointer, entries a row, row stride) of the page tables of n sequences."""
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n or table.shape[1] < 1:
-        raise ValueError(f"table must be an int32 [{n}, pages] tensor, not {table.dtype} {list(table.shape)}")
+    shape = table.shape
+    if table.dtype is not _INT32 or len(shape) != 2 or shape[0] != n or shape[1] < 1:
+        raise ValueError(f"table must be an int32 [{n}, pages] tensor, not {table.dtype} {list(shape)}")
     ld, step = table.stride()
-    width = table.shape[1]
+    width = shape[1]
     if (step != 1 and width > 1) or (n > 1 and ld < width):
         raise ValueError("table needs a contiguous last dimension and rows that do not overlap")
     if table.get_device() != dev:
@@ -625,10 +632,12 @@ def _cache(cache: torch.Tensor, layout: moe_kv_layout, dev: int) -> int:
     return cache.data_ptr()
 
 
-def _heads_of(q: torch.Tensor, layout: moe_kv_layout, what: str) -> int:
-    if q.dim() != 2 or q.shape[1] < 1 or q.shape[1] % layout.head:
-        raise ValueError(f"{what} must be [rows, heads * {layout.head}], not {list(q.shape)}")
-    return q.shape[1] // layout.head
+def _heads_of(q: torch.Tensor, head: int, what: str):
+    """(rows, width, heads) of query rows."""
+    shape = q.shape
+    if len(shape) != 2 or shape[1] < 1 or shape[1] % head:
+        raise ValueError(f"{what} must be [rows, heads * {head}], not {list(shape)}")
+    return shape[0], shape[1], shape[1] // head
 
 
 def moe_kv_plan(length: torch.Tensor, grow: torch.Tensor, layout: moe_kv_layout, table: torch.Tensor,
@@ -659,12 +668,12 @@ def moe_kv_append(k: torch.Tensor, v: torch.Tensor, layout: moe_kv_layout, cache
     dev, t, width = k.get_device(), k.shape[0], layout.heads * layout.head
     kp, xt, ldk = _row_args(k, t, width, dev, "k")
     vp, vt, ldv = _row_args(v, t, width, dev, "v")
-    qp, qt, ldq, qop, qot, ldqo, hq = None, xt, 0, None, BF16, 0, 0
+    qp, qt, ldq, qop, qot, ldqo, wq, hq = None, xt, 0, None, BF16, 0, layout.head, 0
     if q is not None:
-        hq = _heads_of(q, layout, "q")
-        qp, qt, ldq = _row_args(q, t, hq * layout.head, dev, "q")
+        _, wq, hq = _heads_of(q, layout.head, "q")
+        qp, qt, ldq = _row_args(q, t, wq, dev, "q")
     if q_out is not None:
-        qop, qot, ldqo = _row_args(q_out, t, (hq or 1) * layout.head, dev, "q_out")
+        qop, qot, ldqo = _row_args(q_out, t, wq, dev, "q_out")
     if vt != xt or qt != xt or qot != BF16:
         raise ValueError("k, v and q must have one type, q_out is bfloat16")
     rp, rows, rot = None, 0, 0
@@ -683,15 +692,15 @@ def moe_attention_workspace_bytes(t: int, n: int, heads_q: int, layout: moe_kv_l
 
 
 def _attention_args(q, layout, cache, table, n, length, out, workspace):
-    dev, t, hq = q.get_device(), q.shape[0], _heads_of(q, layout, "q")
-    qp, qt, ldq = _row_args(q, t, hq * layout.head, dev, "q")
-    op, ot, ldo = _row_args(out, t, hq * layout.head, dev, "out")
+    dev, (t, width, hq) = q.get_device(), _heads_of(q, layout.head, "q")
+    qp, qt, ldq = _row_args(q, t, width, dev, "q")
+    op, ot, ldo = _row_args(out, t, width, dev, "out")
     if qt != BF16 or ot != BF16:
         raise ValueError("q and out must be bfloat16")
-    tp, width, ldt = _table_args(table, n, dev)
+    tp, pages, ldt = _table_args(table, n, dev)
     if not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous, on the GPU of the other tensors")
-    return (dev, t, hq, qp, ldq, _cache(cache, layout, dev), tp, width, ldt, _ints(length, n, dev, "length"), op, ldo,
+    return (dev, t, hq, qp, ldq, _cache(cache, layout, dev), tp, pages, ldt, _ints(length, n, dev, "length"), op, ldo,
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
