@@ -565,12 +565,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     const int krow = (m & 0x13) | (m & 4) << 1 | (m & 8) >> 1;
     constexpr uint64_t ALL = TK == 64 ? ~0ull : (1ull << 32) - 1;
     typedef f32x16 Scores[NB];
-    // operand x of a tile's products, in their order: of the scores (block of 32 tokens, 16 columns), of the outputs
-    // (16 tokens, block of 32 columns)
+    // operand x of a tile's products, in their order: of the scores (16 columns, block of 32 tokens), of the outputs
+    // (16 tokens, block of 32 columns), so that neighbouring products add to different sums
     constexpr int NK = NB * NKS, NV = NVS * ND;
     const uint8_t *const k_lane = tile_lds + (hf * TK + krow) * 16, *const v_lane = tile_lds + 2 * TB + (hf * D + m) * 16;
     auto key_frag = [&](int kt, int x) {
-        return *reinterpret_cast<const bf16x8 *>(k_lane + (kt & 1) * TB + x % NKS * (2 * TK * 16) + x / NKS * 512);
+        return *reinterpret_cast<const bf16x8 *>(k_lane + (kt & 1) * TB + x / NB * (2 * TK * 16) + x % NB * 512);
     };
     auto value_frag = [&](int kt, int x) {
         return *reinterpret_cast<const bf16x8 *>(v_lane + (kt & 1) * TB + x / ND * (2 * D * 16) + x % ND * 512);
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
         for (int j = 0; j < 16; ++j) s[b][j] = 0.0f;
     };
     auto score = [&](Scores &s, const bf16x8 &kf, int x) {
-        s[x / NKS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x % NKS], s[x / NKS], 0, 0, 0);
+        s[x % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x / NB], s[x % NB], 0, 0, 0);
     };
     // no score for tokens that are not there or come after the row (there: the tile's tokens that are)
     auto mask = [&](Scores &s, int kt, uint64_t there) {
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
 #pragma unroll
             for (int x = 0; x < NK; ++x) {
                 __builtin_amdgcn_sched_barrier(0);
-                if (x % NKS == 0) zero(n, x / NKS);
+                if (x < NB) zero(n, x);
                 score(n, f[x % AHEAD], x);
                 f[x % AHEAD] = x + AHEAD < NK ? key_frag(kt + 1, x + AHEAD) : value_frag(kt, x + AHEAD - NK);
                 if (!E4M3)
