@@ -627,6 +627,9 @@ moe_status moe_residual_norm(const void *x, int32_t x_type, int64_t ldx, const v
  *   v   [pages][heads][page / C][head][C]                  a cell is C tokens' values of one column
  *   ks, vs  u8 [pages][heads][page]                        e4m3 only
  *
+ * Attention may take values below 2^-126, and e4m3 heads whose largest value
+ * is below 2^-118, as 0.  No scale byte of a token that is there is 255.
+ *
  * moe_kv_layout_make fills *out [host] for 1 <= pages <= 2^24, page 16, 32,
  * 64, 128 or 256, pages * page <= 2^30, 1 <= heads <= 256, head 64, 128 or
  * 256, type MOE_BF16 or MOE_E4M3; MOE_ERR_INVALID otherwise.  Sections are

@@ -208,7 +208,10 @@ __device__ __forceinline__ void leave_info(const AttentionArgs &a, const Unit &u
 // turn, each for itself, straight from the cache into the matrix core's
 // operands, and add up their outputs in LDS at the end.  The weights enter the
 // second product as two bf16 terms, p = hi + lo, which costs nothing where
-// memory is the bound.  Bound by memory.
+// memory is the bound.  Bound by memory: 32 sequences of 16000 tokens, 32 / 8
+// heads of 128, 359 us, 5.7 TB/s, 96% of a streaming read.  (The next tile's
+// operands in registers while one is used made no difference: eight or twelve
+// waves a CU have enough on the way.)
 template <int CT, int D, bool SMALL>
 __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16 ? 2 : 1) k_decode(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;
@@ -442,7 +445,11 @@ __device__ __forceinline__ bool not_finite(u32x4 w) {
 //
 // A wave computes the scores of tile t + 1 while it turns those of tile t into
 // weights, so that the matrix core and the vector units are both busy; keys
-// are therefore fetched two tiles ahead, values one.
+// are therefore fetched two tiles ahead, values one.  Bound by the vector units
+// beside the matrix core (39% and 44% of the cycles busy): 4096 rows, 32 / 8 heads
+// of 128, 147 us, 930 TFLOP/s (one tile's steps in turn: 178); heads of 256, with
+// one wave a SIMD and all its registers, 149 us for as many operations (in the
+// 256 of two waves they spill: 245).
 template <int CT, int D, bool SMALL>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;

@@ -254,16 +254,23 @@ __device__ __forceinline__ uint2 codes8(const float v[8], float inv) {
     return make_uint2(lo, hi);
 }
 
+// Workgroup b's unit, where each of the 8 XCDs (to which workgroups go in turn)
+// takes one run of the units.
+__device__ __forceinline__ int xcd_unit(int b, int n) {
+    const int xcd = b % 8, each = n / 8, more = n % 8;  // the first `more` runs have one unit more
+    return xcd * each + min(xcd, more) + b / 8;
+}
+
 // A workgroup takes 4096 / D consecutive rows of one head of q, k or v
-// (blockIdx.x: the heads of q, then of k, then of v, so that what runs together
-// reads whole rows); a thread two cells of 8 values of a row, of what is rotated
+// (the heads of q, then of k, then of v, then the next rows, so that what runs
+// together on an XCD reads whole rows); a thread two cells of 8 values of a row, of what is rotated
 // the two halves of 8 pairs, so that a rotation needs no other lane.  Keys and values turn in LDS, so that neighbouring lanes write
 // neighbouring cells: keys 16 bytes a lane, the rows of a column of cells
 // beside each other; values, which stand by columns, 8 rows of a column at
 // once where those have 8 neighbouring slots, otherwise one by one.
-// Bound by memory: 4096 rows of 32 + 8 + 8 heads of 128, 102 MB, 29.7
-// us (a copy of as many bytes 21; with a thread's pair half a row away, rows
-// fastest in the grid and keys written 16 bytes a row 34.7).
+// Bound by memory: 4096 rows of 32 + 8 + 8 heads of 128, 102 MB, 29.0
+// us (a copy of as many bytes 21; without the runs of XCDs 29.7; with a thread's
+// pair half a row away, rows fastest in the grid and keys written 16 bytes a row 34.7).
 template <int XT, int CT, int D>
 __global__ void __launch_bounds__(256) k_kv_append(KvAppendArgs a) {
     constexpr int LANES = D / 16, ROWS = 256 / LANES, SIZE = CT == MOE_BF16 ? 2 : 1, CELL = 16 / SIZE;
@@ -271,8 +278,9 @@ __global__ void __launch_bounds__(256) k_kv_append(KvAppendArgs a) {
     __shared__ __align__(16) uint8_t turn[ROWS * STRIDE];
     __shared__ int slots[ROWS];  // -1: not stored
     const KvCache &c = a.c;
-    const int tid = threadIdx.x, mine = tid % LANES, in = tid / LANES, row0 = (int)blockIdx.y * ROWS, row = row0 + in;
-    int head = blockIdx.x;
+    const int tid = threadIdx.x, mine = tid % LANES, in = tid / LANES, unit = xcd_unit(blockIdx.x, gridDim.x);
+    const int all = a.heads_q + 2 * c.heads, row0 = unit / all * ROWS, row = row0 + in;
+    int head = unit % all;
     const int what = head < a.heads_q ? 0 : head < a.heads_q + c.heads ? 1 : 2;  // q, k, v
     head -= what == 0 ? 0 : what == 1 ? a.heads_q : a.heads_q + c.heads;
     const int page = 1 << c.shift, tokens = c.pages << c.shift;
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(256) k_kv_append(KvAppendArgs a) {
 template <int XT, int CT>
 hipError_t launch_append(const KvAppendArgs &a, hipStream_t s) {
     const int rows = 4096 / a.c.head;
-    const dim3 grid(a.heads_q + 2 * a.c.heads, (a.t + rows - 1) / rows);
+    const dim3 grid((a.heads_q + 2 * a.c.heads) * ((a.t + rows - 1) / rows));
     if (a.c.head == 64) hipLaunchKernelGGL((k_kv_append<XT, CT, 64>), grid, dim3(256), 0, s, a);
     else if (a.c.head == 128) hipLaunchKernelGGL((k_kv_append<XT, CT, 128>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_kv_append<XT, CT, 256>), grid, dim3(256), 0, s, a);
