@@ -1,6 +1,6 @@
 // Attention over the paged key-value cache on gfx950: one row a sequence
 // (k_decode) and a chunk's packed rows (k_prefill), and the joining of
-// sequences that several workgroups share (k_join).
+// sequences that several workgroups share (k_join_rows, k_join_tiles).
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m)
 //
@@ -39,16 +39,31 @@ constexpr float kMostSlack = 1e38f;    // finite, so that the first score sets t
 // How many tokens a part has: as many as make `few` units of all tiles, but
 // from `least` to `enough`; and at least as many as make `many` units.  The
 // chip holds 512 workgroups at a time (256 of heads of 256).  Decode: with
-// {512, 128, 1024, 2048} one sequence of 1000 tokens takes 8.4 us and one of
-// 32000 35 us (2048 units of 128 and more: 10.3 and 45), 32 of 16000 359 (1024:
-// 363).  Prefill: more than 512 units were slower wherever tiles were cut.  A
-// full tile's part costs 66 KB written and read again, so such tiles have parts
-// of twice `least` (512 rows of one sequence 23.4 -> 18.8 us); tiles of few
-// rows gain from shorter ones (64 rows after 4 x 2000 tokens 18.9 -> 15.9).
+// {512, 128, 1024, 2048} one sequence of 1000 tokens takes 7.7 us and one of
+// 32000 36 us (2048 units of 128 and more: 10.3 and 45), 32 of 16000 359 (1024:
+// 363).  Prefill: more than 512 units were slower wherever tiles were cut.
 struct Cut {
     int few, least, enough, many;
 };
 constexpr Cut kDecodeCut = {512, 128, 1024, 2048}, kPrefillCut = {256, 256, 1024, 512};
+// Where no sequence can have more tokens than this, nothing is cut and the
+// joining launch left out: decode of 200 tokens 7.5 -> 5.2 us, of 440 7.6 ->
+// 7.0, prefill of 440 rows 17.1 -> 15.5; 1 row after 440 tokens 11.8 -> 12.6.
+constexpr int kUncut = 512;
+// The least that a part of a sequence of several tiles has: a full tile's part
+// costs 66 KB written and read again (512 rows 23.4 -> 18.8 us; tiles of few
+// rows gain from shorter ones, 64 rows after 4 x 2000 tokens 18.9 -> 15.9).
+// Where rows are at least half of the tokens, tiles of all lengths fill the
+// chip by themselves from kWholeTiles (tile, key head)s on: prompts of 800,
+// 1200 and 1600 rows 29.4, 40.8, 55.3 -> 24.8, 33.0, 42.1 us; with half as many
+// key heads (128 for 2048 rows) 33.3 -> 43.5, and 300 rows each after 3 x 2000
+// tokens 22.1 -> 29.6, so not there.
+constexpr int kLeastTiles = 512, kLeastWhole = 2048, kWholeTiles = 200;
+// At most so many (row, query head)s are joined by a workgroup each, more by
+// tiles: 64 rows of 32 heads after 4 x 2000 tokens 15.6 (by tiles 19.6), 1 row
+// after 8000 14.8 (42.6); 1000 rows after 4 x 1000 26.6 (23.3), 1024 after
+// 16 x 1000, e4m3, 49.9 (42.6).
+constexpr int kWideItems = 4096;
 
 __device__ __forceinline__ float minus_inf() { return -__builtin_inff(); }
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
@@ -90,14 +105,14 @@ __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) 
     q.len = min(max(a.length[s], 0), a.max_tokens);
     q.first = s;
     q.rows = q.tiles = 1;
-    q.least = PREFILL ? kPrefillCut.least : kDecodeCut.least;
+    q.least = a.least;
     if (PREFILL || a.starts) {
         const int end = min(max(a.starts[s + 1], 0), a.t);
         q.first = min(max(a.starts[s], 0), a.t);
         q.rows = max(end - q.first, 0);
         q.tiles = PREFILL ? (q.rows * group + kPrefillRows - 1) / kPrefillRows : min(q.rows, 1);
         if (!PREFILL) q.first = end - 1;
-        if (PREFILL && q.tiles > 1) q.least *= 2;
+        if (PREFILL && q.tiles > 1) q.least = max(q.least, 2 * q.rows >= q.len ? a.least_whole : kLeastTiles);
     }
     return q;
 }
@@ -194,11 +209,16 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
     return true;
 }
 
-// What the joining launch has to know, of a sequence from its first unit, and
-// whether there is anything to join from the call's first.
+// What the joining launch has to know: first of all how many partial results
+// a head has, then by sequence its parts and where they start, or (by_tile) by
+// partial result that is a tile's first the tile's parts, its sequence's first
+// row and rows, and the tile (parts 0: not a first one).
 __device__ __forceinline__ void leave_info(const AttentionArgs &a, const Unit &u, int head_tile) {
-    if (threadIdx.x == 0 && head_tile == 0 && u.tile == 0 && u.part == 0) a.info[u.s] = make_int2(u.split, u.slot);
-    if (threadIdx.x == 0 && blockIdx.x == 0) a.info[a.n] = make_int2(u.cuts, 0);
+    if (threadIdx.x != 0) return;
+    if (blockIdx.x == 0) a.info[0] = make_int4(u.cuts, 0, 0, 0);
+    if (head_tile) return;
+    if (a.by_tile && u.split > 1) a.info[1 + u.slot] = make_int4(u.part ? 0 : u.split, u.first, u.rows, u.tile);
+    if (!a.by_tile && u.tile == 0 && u.part == 0) a.info[1 + u.s] = make_int4(u.split, u.slot, 0, 0);
 }
 
 // ------------------------------------------------------------------ one row a sequence
@@ -824,9 +844,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
         if (kt + 1 < t1) step(sb, sa, kt + 1);
     }
     lds::wait_vm<0>();  // the last fetches (of no tile) may not outlive the workgroup's LDS
-    if (!live) return;
+    if (!wave_live) return;
     l += __shfl_xor(l, 32, 64);
     if (u.split == 1) {
+        if (!live) return;
         const size_t at = (size_t)(u.first + token) * a.ldo + (size_t)(h * G + x % G) * D;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -835,7 +856,16 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
             for (int j = 0; j < 16; j += 4)
                 *reinterpret_cast<uint2 *>(a.out + at + 32 * i + 2 * j + 4 * hf) =
                     make_uint2(pk_bf16(o[i][j] * inv, o[i][j + 1] * inv), pk_bf16(o[i][j + 2] * inv, o[i][j + 3] * inv));
-    } else {
+    } else if (a.by_tile) {  // as the registers are, which is how the joining launch reads them
+        const size_t block = ((size_t)u.slot * H + h) * (a.part_rows / 32) + wave;
+        if (hf == 0) a.stats[block * 32 + m] = make_float2(mx * cs, l);
+        f32x4 *part = reinterpret_cast<f32x4 *>(a.part) + block * (ND * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                part[(i * 4 + j) * 64] = (f32x4){o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+    } else if (live) {
         const size_t at = ((size_t)u.slot * H + h) * a.part_rows + wave * 32 + m;
         if (hf == 0) a.stats[at] = make_float2(mx * cs, l);
 #pragma unroll
@@ -848,6 +878,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
 }
 
 // ------------------------------------------------------------------ joining
+
+// Partial outputs are weighted by 2^(m - largest m) and divided by the sum of
+// the sums weighted so, in order.  Bound by the parts' bytes, or by latency.
+__device__ __forceinline__ float part_weight(float m, float top) {
+    return m == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+}
 
 // Where the parts of a (row, query head) stand: slots slot0 .. slot0 + split - 1
 // at row `in` of head tile ht; false if it was not cut, or is no sequence's.
@@ -879,34 +915,33 @@ __device__ __forceinline__ bool parts_of(const AttentionArgs &a, int r, int hq, 
         p.ht = hq / G * QT + hq % G / kDecodeRows;
         p.in = hq % G % kDecodeRows;
     }
-    const int2 info = a.info[s];
+    const int4 info = a.info[1 + s];
     p.split = info.x;
     p.slot0 = info.y + tile * p.split;
     return p.split >= 2 && p.slot0 >= 0 && p.slot0 <= a.slots - p.split;
 }
 
-// The parts of rows whose tiles were cut: outputs weighted by 2^(m - largest
-// m), over the sum of the weights, in order.  A wave a (row, query head), or
-// where those are few and may have hundreds of parts (WIDE) a workgroup, whose
-// waves take runs of them: 1 row x 32 heads of 32 parts, prefill, 23.1 -> 16.2 us.
-// Bound by the parts' bytes, or by latency.
+// A wave a (row, query head), or where those are few and may have hundreds of
+// parts (WIDE) a workgroup, whose waves take runs of them: 1 row x 32 heads of
+// 32 parts, prefill, 23.1 -> 16.2 us.
 template <bool PREFILL, int D, bool WIDE>
-__global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
+__global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
     constexpr int V = D / 64;  // columns a lane
     typedef float vec __attribute__((ext_vector_type(V)));
     __shared__ vec wave_sum[WIDE ? 3 : 1][64];
     __shared__ float wave_l[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, H = a.c.heads, G = a.heads_q / H;
     const int QT = PREFILL ? 1 : (G + kDecodeRows - 1) / kDecodeRows, HT = H * QT;
-    if (a.info[a.n].x == 0) return;
+    if (a.info[0].x == 0) return;
     const int rows = PREFILL ? min(max(a.starts[a.n], 0), a.t) : a.n;
     const int step = WIDE ? gridDim.x : gridDim.x * 4;
     for (int item = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave; item < rows * a.heads_q; item += step) {
         const int hq = item % a.heads_q;
         Parts p;
         if (!parts_of<PREFILL>(a, item / a.heads_q, hq, G, QT, p)) continue;  // (WIDE: for all four waves)
+        const int split = p.split;
         auto place = [&](int i) { return ((size_t)(p.slot0 + i) * HT + p.ht) * a.part_rows + p.in; };
-        const int each = (p.split + 3) / 4, i0 = WIDE ? wave * each : 0, i1 = WIDE ? min(i0 + each, p.split) : p.split;
+        const int each = (split + 3) / 4, i0 = WIDE ? wave * each : 0, i1 = WIDE ? min(i0 + each, split) : split;
         // the first parts are asked for before the maximum is known
         constexpr int FIRST = WIDE ? 8 : 4;
         vec part[FIRST];
@@ -914,9 +949,9 @@ __global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
         for (int i = 0; i < FIRST; ++i)
             if (i0 + i < i1) part[i] = *reinterpret_cast<const vec *>(a.part + place(i0 + i) * D + lane * V);
         float2 mine = make_float2(minus_inf(), 0.0f);  // part `lane` of the first 64
-        if (lane < p.split) mine = a.stats[place(lane)];
+        if (lane < split) mine = a.stats[place(lane)];
         float top = mine.x;
-        for (int i = lane + 64; i < p.split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
+        for (int i = lane + 64; i < split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
         vec sum;
@@ -925,7 +960,7 @@ __global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
         float l = 0.0f;
         auto add = [&](int i, vec v) {
             const float2 st = i < 64 ? make_float2(__shfl(mine.x, i, 64), __shfl(mine.y, i, 64)) : a.stats[place(i)];
-            const float f = st.x == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
+            const float f = part_weight(st.x, top);
             l += f * st.y;
             sum += f * v;
         };
@@ -956,6 +991,49 @@ __global__ void __launch_bounds__(256) k_join(AttentionArgs a) {
     }
 }
 
+// by_tile: a workgroup 32 columns of a tile of a key head, a wave 32 of its
+// rows, each lane what its lane of the parts' waves had.
+template <int D>
+__global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
+    constexpr int ND = D / 32;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 31, hf = lane >> 5;
+    const int H = a.c.heads, G = a.heads_q / H;
+    const int items = min(a.info[0].x, a.slots) * H * ND;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int i = item % ND, h = item / ND % H, slot = item / ND / H;
+        const int4 info = a.info[1 + slot];
+        const int split = info.x, first = info.y, rows = info.z, x0 = info.w * kPrefillRows + wave * 32, x = x0 + m;
+        // (starts in no order may leave entries of other calls)
+        if (split < 2 || split > a.slots - slot || first < 0 || rows < 1 || rows > a.t - first || info.w < 0 ||
+            info.w > rows * G / kPrefillRows || x0 >= rows * G)
+            continue;
+        const size_t step = (size_t)H * (a.part_rows / 32), block = ((size_t)slot * H + h) * (a.part_rows / 32) + wave;
+        const float2 *stats = a.stats + block * 32 + m;
+        const f32x4 *part = reinterpret_cast<const f32x4 *>(a.part) + (block * ND + i) * (4 * 64) + lane;
+        float top = minus_inf();
+        for (int p = 0; p < split; ++p) top = fmaxf(top, stats[p * step * 32].x);
+        f32x4 sum[4];
+        float l = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = (f32x4){0, 0, 0, 0};
+#pragma unroll 4
+        for (int p = 0; p < split; ++p) {
+            const float2 st = stats[p * step * 32];
+            const float f = part_weight(st.x, top);
+            l += f * st.y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] += f * part[p * step * (ND * 4 * 64) + j * 64];
+        }
+        if (x >= rows * G) continue;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *to = a.out + (size_t)(first + x / G) * a.ldo + (size_t)(h * G + x % G) * D + 32 * i + 4 * hf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint2 *>(to + 8 * j) =
+                make_uint2(pk_bf16(sum[j].x * inv, sum[j].y * inv), pk_bf16(sum[j].z * inv, sum[j].w * inv));
+    }
+}
+
 template <int CT, int D>
 hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
     const int G = a.heads_q / a.c.heads;
@@ -965,7 +1043,7 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
     const int tiles = prefill ? a.t * G / kPrefillRows + a.n : a.n;
     const Cut cut = prefill ? kPrefillCut : kDecodeCut;
     // no more units of a head than the cuts make, and a unit a tile; nor than the tables' tokens allow
-    const int64_t most = (int64_t)tiles * ((a.max_tokens + cut.least - 1) / cut.least);
+    const int64_t most = (int64_t)tiles * ((a.max_tokens + a.least - 1) / a.least);
     const int units = (int)(most < cut.many / HT + tiles ? most : cut.many / HT + tiles);
     const dim3 grid((unsigned)(units * HT)), block(256);
     const bool few = a.n <= 64;
@@ -977,16 +1055,19 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
         else hipLaunchKernelGGL((k_decode<CT, D, false>), grid, block, 0, s, a);
     }
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.max_tokens <= cut.least) return hipSuccess;  // nothing is cut
-    // 2048 workgroups fill the chip; more items are taken in turn
+    if (a.max_tokens <= a.least) return hipSuccess;  // nothing is cut
+    // workgroups that fill the chip; more items are taken in turn
+    if (a.by_tile) {
+        hipLaunchKernelGGL((k_join_tiles<D>), dim3(2048), block, 0, s, a);
+        return hipGetLastError();
+    }
     const int64_t items = (int64_t)(prefill ? a.t : a.n) * a.heads_q;
-    const bool wide = items <= 4096;
+    const bool wide = items <= kWideItems;
     const int64_t blocks = wide ? items : (items + 3) / 4;
     const dim3 join((unsigned)(blocks < 2048 ? blocks : 2048));
-    if (prefill && wide) hipLaunchKernelGGL((k_join<true, D, true>), join, block, 0, s, a);
-    else if (prefill) hipLaunchKernelGGL((k_join<true, D, false>), join, block, 0, s, a);
-    else if (wide) hipLaunchKernelGGL((k_join<false, D, true>), join, block, 0, s, a);
-    else hipLaunchKernelGGL((k_join<false, D, false>), join, block, 0, s, a);
+    if (prefill) hipLaunchKernelGGL((k_join_rows<true, D, true>), join, block, 0, s, a);
+    else if (wide) hipLaunchKernelGGL((k_join_rows<false, D, true>), join, block, 0, s, a);
+    else hipLaunchKernelGGL((k_join_rows<false, D, false>), join, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -1013,14 +1094,18 @@ AttentionPlan attention_plan(bool prefill, int t, int n, int heads_q, int heads,
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t rows = (size_t)p.slots * HT * p.part_rows;
     p.info = 0;
-    p.stats = up(((size_t)n + 1) * sizeof(int2));
+    p.stats = up(((size_t)(prefill && p.slots > n ? p.slots : n) + 1) * sizeof(int4));
     p.part = p.stats + up(rows * sizeof(float2));
     p.total = p.part + up(rows * head * sizeof(float));
     return p;
 }
 
-hipError_t launch_attention(const AttentionArgs &a, hipStream_t s) {
+hipError_t launch_attention(const AttentionArgs &args, hipStream_t s) {
     ProfileScope ps(MOE_PHASE_ATTENTION, s);
+    AttentionArgs a = args;
+    a.least = a.max_tokens <= kUncut ? kUncut : a.prefill ? kPrefillCut.least : kDecodeCut.least;
+    a.least_whole = (int64_t)a.t * a.heads_q >= (int64_t)kWholeTiles * kPrefillRows ? kLeastWhole : kLeastTiles;
+    a.by_tile = a.prefill && (int64_t)a.t * a.heads_q > kWideItems;
     return a.c.type == MOE_BF16 ? launch_head<MOE_BF16>(a, s) : launch_head<MOE_E4M3>(a, s);
 }
 

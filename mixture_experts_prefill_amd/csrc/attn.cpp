@@ -96,7 +96,7 @@ moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t
     a.scale = scale;
     a.prefill = prefill;
     char *w = static_cast<char *>(workspace);
-    a.info = reinterpret_cast<int2 *>(w + p.info);
+    a.info = reinterpret_cast<int4 *>(w + p.info);
     a.stats = reinterpret_cast<float2 *>(w + p.stats);
     a.part = reinterpret_cast<float *>(w + p.part);
     a.part_rows = p.part_rows;

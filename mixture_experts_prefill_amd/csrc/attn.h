@@ -52,11 +52,15 @@ struct AttentionArgs {
     const int32_t *table, *length, *starts;  // starts: null if row s is sequence s's (decode)
     int64_t ldq, ldo, ldt;
     int t, n, heads_q, max_tokens;
+    // set by the launcher: tokens of a part at the least, and of a whole prompt
+    // of several tiles; whether tiles are joined, or rows
+    int least, least_whole;
+    bool by_tile;
     float scale;
     bool prefill;
-    // workspace: per sequence its split and first partial slot; partial sums
-    // [slot][head tile][part_rows][head] and their (maximum, sum) pairs
-    int2 *info;
+    // workspace: what the joining launch has to know; partial outputs of
+    // [slot][head tile] part_rows rows, and their (maximum, sum) pairs
+    int4 *info;
     float *part;
     float2 *stats;
     int part_rows;   // rows that a partial result has room for

@@ -193,6 +193,24 @@ def test_prefill_cut_along_its_tokens(mep, lengths, rows, dtype):
         prefill(mep, Batch(mep, lengths, heads, head, 64, dtype), rows, hq, (lengths, heads, head, dtype))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads,g,head", [(2, 11, 64), (2, 8, 128), (1, 16, 256)])
+@pytest.mark.parametrize("lengths,rows", [([1000], [900]), ([1700, 0, 2300], [300, 0, 333]), ([5000, 700, 3], [257, 1, 1])])
+def test_prefill_joins_tiles(mep, lengths, rows, heads, g, head, dtype):
+    """More rows than are joined one by one: tiles of full, few and no rows, sequences that start between tiles."""
+    b = Batch(mep, lengths, heads, head, 32, dtype, seed=sum(rows) + g)
+    prefill(mep, b, rows, heads * g, f"prefill {lengths} {rows} {heads}x{g}x{head}")
+
+
+@pytest.mark.parametrize("tokens", [479, 480, 481, 512])
+def test_tables_about_the_length_that_is_cut(mep, tokens):
+    """The tables' widths, not the lengths, say whether a joining launch follows: 512 tokens here up to 480."""
+    for page, least in ((16, 1), (32, tokens - 1)):
+        b = Batch(mep, [tokens, least], 2, 128, page, BF16, seed=tokens)
+        decode(mep, b, 8, f"decode {tokens}")
+        prefill(mep, b, [tokens // 2, least], 8, f"prefill {tokens}")
+
+
 @pytest.mark.parametrize("n", [64, 65, 256, 300])
 def test_prefill_many_sequences(mep, n):
     rnd = random.Random(n)
