@@ -136,6 +136,7 @@ __device__ __forceinline__ int splits(const Seq &q, int tokens) {
 template <bool PREFILL, bool SMALL>
 __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int group, int heads, Unit &u) {
     const int tid = threadIdx.x, lane = tid & 63;
+    u.cuts = 0;
     if (SMALL) {
         Seq q = {0, 0, 0, 0, 1};
         if (lane < a.n) q = seq_of<PREFILL>(a, lane, group);
@@ -199,26 +200,35 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
             }
         }
         __syncthreads();
+        if (found.s < 0) return false;
         u = found;
-        if (u.s < 0) return false;
-        u.cuts = 0;
         for (int w = 0; w < 4; ++w) u.cuts += wave_parts[w];
     }
     // the tiles of a sequence run from its last, which have the most tokens; slots are in the order of the tiles
     u.slot += u.tile * u.split + u.part;
-    return true;
+    // starts in no order may claim more rows than there are: tiles and slots that the workspace was not made for
+    if (PREFILL && (u.tile < 0 || u.tile > (u.rows * group - 1) / kPrefillRows)) return false;
+    return u.split == 1 || (uint32_t)u.slot < (uint32_t)a.slots;
 }
 
-// What the joining launch has to know: first of all how many partial results
+// Unit v, and what the joining launch has to know: first of all how many partial results
 // a head has, then by sequence its parts and where they start, or (by_tile) by
 // partial result that is a tile's first the tile's parts, its sequence's first
 // row and rows, and the tile (parts 0: not a first one).
-__device__ __forceinline__ void leave_info(const AttentionArgs &a, const Unit &u, int head_tile) {
-    if (threadIdx.x != 0) return;
-    if (blockIdx.x == 0) a.info[0] = make_int4(u.cuts, 0, 0, 0);
-    if (head_tile) return;
-    if (a.by_tile && u.split > 1) a.info[1 + u.slot] = make_int4(u.part ? 0 : u.split, u.first, u.rows, u.tile);
-    if (!a.by_tile && u.tile == 0 && u.part == 0) a.info[1 + u.s] = make_int4(u.split, u.slot, 0, 0);
+template <bool PREFILL, bool SMALL>
+__device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int group, int heads, int head_tile, Unit &u) {
+    const bool any = find_unit<PREFILL, SMALL>(a, v, group, heads, u);
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) a.info[0] = make_int4(u.cuts, 0, 0, 0);
+        if (any && head_tile == 0) {
+            if (PREFILL && a.by_tile) {
+                if (u.split > 1) a.info[1 + u.slot] = make_int4(u.part ? 0 : u.split, u.first, u.rows, u.tile);
+            } else if (u.tile == 0 && u.part == 0) {
+                a.info[1 + u.s] = make_int4(u.split, u.slot, 0, 0);
+            }
+        }
+    }
+    return any;
 }
 
 // ------------------------------------------------------------------ one row a sequence
@@ -245,8 +255,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Unit u;
-    if (!find_unit<false, SMALL>(a, blockIdx.x / HT, G, HT, u)) return;
-    leave_info(a, u, ht);
+    if (!take_unit<false, SMALL>(a, blockIdx.x / HT, G, HT, ht, u)) return;
     // parts of equal numbers of tiles
     const int tiles = (u.len + TK - 1) / TK, each = (tiles + u.split - 1) / u.split;
     const int t0 = u.part * each, t1 = min(t0 + each, tiles);
@@ -479,8 +488,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     const KvCache &c = a.c;
     const int G = a.heads_q / c.heads, H = c.heads, h = blockIdx.x % H;
     Unit u;
-    if (!find_unit<true, SMALL>(a, blockIdx.x / H, G, H, u)) return;
-    leave_info(a, u, h);
+    if (!take_unit<true, SMALL>(a, blockIdx.x / H, G, H, h, u)) return;
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, hf = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(tile_lds));
@@ -1003,7 +1011,7 @@ __global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
         const int i = item % ND, h = item / ND % H, slot = item / ND / H;
         const int4 info = a.info[1 + slot];
         const int split = info.x, first = info.y, rows = info.z, x0 = info.w * kPrefillRows + wave * 32, x = x0 + m;
-        // (starts in no order may leave entries of other calls)
+        // (starts in no order: entries may be another call's)
         if (split < 2 || split > a.slots - slot || first < 0 || rows < 1 || rows > a.t - first || info.w < 0 ||
             info.w > rows * G / kPrefillRows || x0 >= rows * G)
             continue;

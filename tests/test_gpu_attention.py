@@ -292,6 +292,48 @@ def test_lengths_and_starts_out_of_range(mep, single):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("g,n", [(1, 18), (5, 6)])
+def test_starts_in_no_order_stay_inside_the_workspace(mep, g, n):
+    """Every other sequence claims all rows: 576 or 600 partial results, 537 and 557 of which have room."""
+    t, length, page = 1000, 24000, 256
+    L = mep.moe_kv_layout_make(94, page, 1, 64, BF16)
+    cache = torch.zeros(L.bytes, dtype=torch.uint8, device="cuda")
+    table = torch.arange(94, dtype=torch.int32, device="cuda").repeat(n, 1)
+    size = mep.moe_attention_workspace_bytes(t, n, g, L)
+    ws = torch.full((size + (64 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    q = torch.randn(t, g * 64, device="cuda").to(BF16)
+    buf, out = guarded(t, g * 64)
+    mep.moe_attention_prefill(q, ints([0, t] * (n // 2) + [0]).cuda(), L, cache, table, ints([length] * n).cuda(),
+                              0.125, out, ws[:size])
+    torch.cuda.synchronize()
+    assert bool((ws[size:] == 0x5a).all()) and intact(buf, t, g * 64)
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("n", [1, 80])
+def test_a_step_without_rows_after_one_that_was_joined(mep, single, n):
+    """The same workspace: nothing that the first call left in it is joined again."""
+    b = Batch(mep, [3000] + [1] * (n - 1), 1, 64, 64, BF16)
+    hq, t = 16, 900
+    q = b.queries(t, hq).cuda()
+    cache, table, length = b.on_gpu()
+    ws = workspace(mep, t, n, hq, b.layout)
+    call = mep.moe_attention_decode if single else mep.moe_attention_prefill
+
+    def step(starts):
+        out, starts = torch.full((t, hq * 64), GUARD, dtype=BF16, device="cuda"), ints(starts).cuda()
+        rest = (b.layout, cache, table, length, 0.125, out, ws)
+        call(q, *rest, starts=starts) if single else call(q, starts, *rest)
+        torch.cuda.synchronize()
+        return out
+
+    first = step([0, 800] + [800] * (n - 1))
+    assert bool((first[799] != GUARD).all())
+    assert bool((step([0] * (n + 1)) == GUARD).all())
+    again = step([0, 5] + [5] * (n - 1))
+    assert bool((again[5:] == GUARD).all() and (again[4] != GUARD).all())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("head", [64, 128, 256])
 def test_values_not_finite_reach_their_readers_only(mep, head, dtype):
