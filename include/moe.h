@@ -731,6 +731,8 @@ size_t moe_attention_workspace_bytes(int32_t t, int32_t n, int32_t heads_q, cons
  * outside 0 .. pages - 1) as not there.  A row without any token is 0, and
  * so is one all of whose scores are minus infinity.
  * Tokens that are not there, whatever their bytes hold, reach no output.
+ * An infinity or NaN in v reaches every row that reads its token, as it is and
+ * however small its weight; two infinities of unequal signs make a NaN.
  *
  *   q      bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
  *   starts NULL: row s is sequence s's, t = n.  Else [n + 1], ascending, 0 .. t: the row of

@@ -19,6 +19,7 @@
 
 #include "attn.h"
 #include "lds_dma.h"
+#include "quant8.h"
 #include "wave_scan.h"
 
 namespace moe {
@@ -231,6 +232,109 @@ __device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int gro
     return any;
 }
 
+// ------------------------------------------------------------------ outputs that are not finite
+
+// A value that is not finite reaches every row that reads its token, as it is
+// (two of unequal signs make NaN), however small the weight.  The matrix
+// products do not give that: 0 times infinity is NaN, and so is infinity
+// times a weight's two terms of unequal signs.  They run as if all values were
+// finite, and an output that then is not is computed here, from the definition:
+//
+//   y = sum_j (w_j / l) v_j over the finite values, or the sum of those that are not
+//
+// 16 lanes a row, a token each: tokens j0 .. j1 - 1 of the sequence whose pages
+// are `pages`, key head h, query row q.  m and l are the row's maximum and sum;
+// columns 4 (lane % 16 + 16 i) .. + 3 are y[i].  No step of the fast path: an
+// output takes as long as the row's products without the matrix core, three times.
+template <int CT, int D>
+__device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const int32_t *pages, int h, const uint16_t *q,
+                                                  int j0, int j1, float cs, float &m, float &l, f32x4 (&y)[D / 64]) {
+    constexpr bool E4M3 = CT == MOE_E4M3;
+    constexpr int SIZE = E4M3 ? 1 : 2, C = 16 / SIZE;  // values a cell
+    const KvCache &c = a.c;
+    const int lane = threadIdx.x & 63, mine = lane & 15, page_mask = (1 << c.shift) - 1;
+    auto page_of = [&](int j) {
+        const int p = j < j1 ? pages[j >> c.shift] : -1;
+        return (unsigned)p < (unsigned)c.pages ? p : -1;
+    };
+    auto block = [&](int p) { return ((size_t)p * c.heads + h) << c.shift; };
+    auto score = [&](int j, int p) {
+        if (p < 0) return minus_inf();
+        const size_t blk = block(p);
+        const int in = j & page_mask;
+        const uint8_t *k = c.k + (blk + (in & ~15)) * (D * SIZE) + (in & 15) * 16;
+        float s = 0.0f;
+#pragma unroll 1
+        for (int d = 0; d < D; d += C) {
+            const u32x4 kw = *reinterpret_cast<const u32x4 *>(k + d / C * 256);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t *qw = reinterpret_cast<const uint32_t *>(q + d) + w * (2 / SIZE);
+                if (E4M3) {
+                    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(kw[w], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(kw[w], true);
+                    s = __builtin_fmaf(lo.x, bf16_lo(qw[0]), s);
+                    s = __builtin_fmaf(lo.y, bf16_hi(qw[0]), s);
+                    s = __builtin_fmaf(hi.x, bf16_lo(qw[1]), s);
+                    s = __builtin_fmaf(hi.y, bf16_hi(qw[1]), s);
+                } else {
+                    s = __builtin_fmaf(bf16_lo(kw[w]), bf16_lo(qw[0]), s);
+                    s = __builtin_fmaf(bf16_hi(kw[w]), bf16_hi(qw[0]), s);
+                }
+            }
+        }
+        return E4M3 ? s * scale_of(c.ks[blk + in], 0) : s;
+    };
+    auto value = [&](int j, int p, int d) {
+        const size_t blk = block(p);
+        const int in = j & page_mask;
+        const uint8_t *v = c.v + (blk + (in & ~(C - 1))) * (D * SIZE) + d * 16 + (in & (C - 1)) * SIZE;
+        if (E4M3) return __builtin_amdgcn_cvt_f32_fp8(*v, 0) * scale_of(c.vs[blk + in], 0);
+        return bf16_lo(*reinterpret_cast<const uint16_t *>(v));
+    };
+    m = minus_inf();
+#pragma unroll 1
+    for (int j = j0 + mine; j < j1; j += 16) m = fmaxf(m, score(j, page_of(j)));
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float top = m == minus_inf() ? 0.0f : m;
+    l = 0.0f;
+#pragma unroll 1
+    for (int j = j0 + mine; j < j1; j += 16) l += __builtin_amdgcn_exp2f((score(j, page_of(j)) - top) * cs);
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    f32x4 wild[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) y[i] = wild[i] = (f32x4){0, 0, 0, 0};
+#pragma unroll 1
+    for (int jb = j0; jb < j1; jb += 16) {
+        const int p = page_of(jb + mine);
+        const float w = __builtin_amdgcn_exp2f((score(jb + mine, p) - top) * cs) * inv;
+#pragma unroll 1
+        for (int x = 0; x < 16; ++x) {
+            const int px = __shfl(p, (lane & 48) + x, 64);
+            const float wx = __shfl(w, (lane & 48) + x, 64);
+            if (px < 0) continue;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = value(jb + x, px, 4 * (mine + 16 * i) + e);
+                    if (q8::finite(v)) y[i][e] = __builtin_fmaf(wx, v, y[i][e]);
+                    else wild[i][e] += v;
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[i][e] = l == 0.0f ? 0.0f : wild[i][e] != 0.0f ? wild[i][e] + 0.0f * l : y[i][e];  // (l: NaN if a score is)
+}
+
+// What a partial result that is not finite gives: itself, also at a weight of 0.
+__device__ __forceinline__ float weighted(float f, float o) { return q8::finite(o) ? f * o : o; }
+
 // ------------------------------------------------------------------ one row a sequence
 
 // A workgroup takes up to 16 query heads of one key head over a run of a
@@ -415,6 +519,9 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
 #pragma unroll
     for (int i = 0; i < VL; ++i) *reinterpret_cast<f32x4 *>(&red[(wave * 16 + m) * D + ((4 * i + g) ^ m) * 4]) = o[i];
     __syncthreads();
+    bool wild = false;
+    auto part_at = [&](int r) { return ((size_t)u.slot * HT + ht) * a.part_rows + r; };
+    auto out_at = [&](int r, int col) { return a.out + u.first * a.ldo + (size_t)(h * G + q0 + r) * D + col * 4; };
     for (int at = threadIdx.x; at < nq * (D / 4); at += 256) {
         const int r = at / (D / 4), col = at % (D / 4);
         float top = red_m[0][r];
@@ -431,12 +538,36 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
         if (u.split == 1) {
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
             sum *= inv;
-            *reinterpret_cast<uint2 *>(a.out + u.first * a.ldo + (size_t)(h * G + q0 + r) * D + col * 4) =
-                make_uint2(pk_bf16(sum.x, sum.y), pk_bf16(sum.z, sum.w));
+            *reinterpret_cast<uint2 *>(out_at(r, col)) = make_uint2(pk_bf16(sum.x, sum.y), pk_bf16(sum.z, sum.w));
         } else {
-            const size_t place = ((size_t)u.slot * HT + ht) * a.part_rows + r;
-            *reinterpret_cast<f32x4 *>(a.part + place * D + col * 4) = sum;
-            if (col == 0) a.stats[place] = make_float2(top * cs, ls);
+            *reinterpret_cast<f32x4 *>(a.part + part_at(r) * D + col * 4) = sum;
+            if (col == 0) a.stats[part_at(r)] = make_float2(top * cs, ls);
+        }
+        wild = wild || !(q8::finite(sum.x) && q8::finite(sum.y) && q8::finite(sum.z) && q8::finite(sum.w));
+    }
+    if (__builtin_expect(!__any(wild), 1)) return;
+    __threadfence_block();  // other lanes wrote what is read below
+    // the rows that this wave wrote above, four at a time: 256 / D of each turn of the loop
+    constexpr int EACH = 256 / D;
+    const int r = wave * EACH + g % EACH + g / EACH * (4 * EACH);
+    if (r >= nq) return;
+    float m_r, l_r;
+    f32x4 y[D / 64];
+    row_by_definition<CT, D>(a, row, h, a.q + u.first * a.ldq + (size_t)(h * G + q0 + r) * D, t0 * TK, min(t1 * TK, u.len),
+                             cs, m_r, l_r, y);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const int col = m + 16 * i;
+        if (u.split == 1) {
+            uint16_t *to = out_at(r, col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((to[e] & 0x7f80) == 0x7f80) to[e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
+        } else {
+            float *to = a.part + part_at(r) * D + col * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!q8::finite(to[e])) to[e] = weighted(a.stats[part_at(r)].y, y[i][e]);
         }
     }
 }
@@ -970,7 +1101,8 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
             const float2 st = i < 64 ? make_float2(__shfl(mine.x, i, 64), __shfl(mine.y, i, 64)) : a.stats[place(i)];
             const float f = part_weight(st.x, top);
             l += f * st.y;
-            sum += f * v;
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] += f == 0.0f ? weighted(f, v[j]) : f * v[j];
         };
 #pragma unroll
         for (int i = 0; i < FIRST; ++i)
