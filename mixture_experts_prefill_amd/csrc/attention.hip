@@ -332,9 +332,6 @@ __device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const 
             y[i][e] = l == 0.0f ? 0.0f : wild[i][e] != 0.0f ? wild[i][e] + 0.0f * l : y[i][e];  // (l: NaN if a score is)
 }
 
-// What a partial result that is not finite gives: itself, also at a weight of 0.
-__device__ __forceinline__ float weighted(float f, float o) { return q8::finite(o) ? f * o : o; }
-
 // ------------------------------------------------------------------ one row a sequence
 
 // A workgroup takes up to 16 query heads of one key head over a run of a
@@ -567,7 +564,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
             float *to = a.part + part_at(r) * D + col * 4;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (!q8::finite(to[e])) to[e] = weighted(a.stats[part_at(r)].y, y[i][e]);
+                if (!q8::finite(to[e])) to[e] = y[i][e] * a.stats[part_at(r)].y;
         }
     }
 }
@@ -594,6 +591,58 @@ __device__ __forceinline__ bool not_finite(u32x4 w) {
     for (int i = 0; i < 4; ++i)
         bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
     return bad;
+}
+
+// What rows that are computed again need of their unit.
+struct Again {
+    int s, first, slot;               // the sequence, its first row, the unit's partial result (-1: none)
+    int x0, pairs, before, j0, j1;    // the tile's first pair, the sequence's pairs, its tokens before its rows, the unit's tokens
+};
+// The outputs of the wave's 32 pairs that are not finite, by definition, in
+// the place of what k_prefill has written.  All that is known of the launch is read
+// anew, so that none of it has to be held in registers along k_prefill's loop
+// (21 scalar registers spilled there, 1000 rows of heads of 256 39.0 -> 40.7 us; so 39.4).
+template <int CT, int D>
+__device__ __forceinline__ void rows_again(const Again &n) {
+    const AttentionArgs *args = reinterpret_cast<const AttentionArgs *>((uintptr_t)__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(args));
+    const AttentionArgs &a = *args;
+    __threadfence_block();  // other lanes wrote what is read below
+    const int H = a.c.heads, G = a.heads_q / H, h = blockIdx.x % H, lane = threadIdx.x & 63, mine = lane % 16;
+    const int32_t *pages = a.table + n.s * a.ldt;
+    const float cs = a.scale * kLog2e;
+    const int x0 = n.x0 + (threadIdx.x >> 6) * 32, rows = min(32, n.pairs - x0);
+    const size_t block = ((size_t)n.slot * H + h) * (a.part_rows / 32) + (threadIdx.x >> 6);
+#pragma unroll 1
+    for (int r = lane / 16; r < rows; r += 4) {  // 16 lanes a pair
+        const int token = (x0 + r) / G, hq = h * G + (x0 + r) % G;
+        uint16_t *out = a.out + (size_t)(n.first + token) * a.ldo + (size_t)hq * D + 4 * mine;
+        // (by_tile: columns 32 i + 8 j + 4 k .. + 3 of a row stand at (4 i + j) * 64 + 32 k + row)
+        const size_t at = a.by_tile ? (block * (D / 8) + mine / 2) * 64 + mine % 2 * 32 + r : (block * 32 + r) * (D / 4) + mine;
+        float *part = a.part + at * 4;
+        const int step = a.by_tile ? 8 * 64 * 4 : 64;  // 64 columns further
+        auto wild = [&](int i, int e) {
+            return n.slot < 0 ? (out[64 * i + e] & 0x7f80) == 0x7f80 : !q8::finite(part[i * step + e]);
+        };
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) any = any || wild(i, e);
+        if (!(__ballot(any) >> (lane & 48) & 0xffff)) continue;
+        float m, l;
+        f32x4 y[D / 64];
+        row_by_definition<CT, D>(a, pages, h, a.q + (size_t)(n.first + token) * a.ldq + (size_t)hq * D, n.j0,
+                                 min(n.j1, n.before + token + 1), cs, m, l, y);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!wild(i, e)) continue;
+                if (n.slot < 0) out[64 * i + e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
+                else part[i * step + e] = y[i][e] * a.stats[block * 32 + r].y;
+            }
+    }
 }
 
 // A workgroup takes 128 (row, query head) pairs of one key head, a wave 32 of
@@ -633,6 +682,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     const int t0 = u.part * each, t1 = min(t0 + each, tiles);
     const int x = xw + m, token = x / G;
     const bool live = x < pairs;
+    __shared__ Again again;
+    if (tid == 0) again = Again{u.s, u.first, u.split > 1 ? u.slot : -1, x0, pairs, before, t0 * TK, min(t1 * TK, u.len)};
     const int pos = live ? before + token : 1 << 30;
     bf16x8 qf[NKS];
     {
@@ -985,18 +1036,26 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     lds::wait_vm<0>();  // the last fetches (of no tile) may not outlive the workgroup's LDS
     if (!wave_live) return;
     l += __shfl_xor(l, 32, 64);
+    f32x4 wild = {0, 0, 0, 0};  // NaN once an output is not finite
+    const float inv = u.split > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            o[i][j] *= inv;
+            wild[j % 4] = __builtin_fmaf(o[i][j], 0.0f, wild[j % 4]);
+        }
+    const size_t block = ((size_t)u.slot * H + h) * (a.part_rows / 32) + wave;
     if (u.split == 1) {
-        if (!live) return;
         const size_t at = (size_t)(u.first + token) * a.ldo + (size_t)(h * G + x % G) * D;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (live)
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
+            for (int i = 0; i < ND; ++i)
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<uint2 *>(a.out + at + 32 * i + 2 * j + 4 * hf) =
-                    make_uint2(pk_bf16(o[i][j] * inv, o[i][j + 1] * inv), pk_bf16(o[i][j + 2] * inv, o[i][j + 3] * inv));
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<uint2 *>(a.out + at + 32 * i + 2 * j + 4 * hf) =
+                        make_uint2(pk_bf16(o[i][j], o[i][j + 1]), pk_bf16(o[i][j + 2], o[i][j + 3]));
     } else if (a.by_tile) {  // as the registers are, which is how the joining launch reads them
-        const size_t block = ((size_t)u.slot * H + h) * (a.part_rows / 32) + wave;
         if (hf == 0) a.stats[block * 32 + m] = make_float2(mx * cs, l);
         f32x4 *part = reinterpret_cast<f32x4 *>(a.part) + block * (ND * 4 * 64) + lane;
 #pragma unroll
@@ -1014,14 +1073,18 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
                 *reinterpret_cast<f32x4 *>(a.part + at * D + 32 * i + 2 * j + 4 * hf) =
                     (f32x4){o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]};
     }
+    if (__builtin_expect(!__any(live && (wild.x + wild.y) + (wild.z + wild.w) != 0.0f), 1)) return;
+    rows_again<CT, D>(again);
 }
 
 // ------------------------------------------------------------------ joining
 
 // Partial outputs are weighted by 2^(m - largest m) and divided by the sum of
 // the sums weighted so, in order.  Bound by the parts' bytes, or by latency.
+// A weight too small for fp32 is its smallest value and not 0, which would make
+// NaN of a part that is infinite.
 __device__ __forceinline__ float part_weight(float m, float top) {
-    return m == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+    return m == minus_inf() ? 0.0f : fmaxf(__builtin_amdgcn_exp2f(m - top), 0x1p-149f);
 }
 
 // Where the parts of a (row, query head) stand: slots slot0 .. slot0 + split - 1
@@ -1101,8 +1164,7 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
             const float2 st = i < 64 ? make_float2(__shfl(mine.x, i, 64), __shfl(mine.y, i, 64)) : a.stats[place(i)];
             const float f = part_weight(st.x, top);
             l += f * st.y;
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] += f == 0.0f ? weighted(f, v[j]) : f * v[j];
+            sum += f * v;
         };
 #pragma unroll
         for (int i = 0; i < FIRST; ++i)

@@ -98,7 +98,7 @@ def test_infinite_values_of_sequences_that_are_cut(mep, lengths, rows, single):
         run(mep, b, rows, hq, head ** -0.5, single, (lengths, heads, head, single))
 
 
-@pytest.mark.parametrize("single", [True])
+@pytest.mark.parametrize("single", [True, False])
 @pytest.mark.parametrize("n", [65, 700, 5000])
 @pytest.mark.parametrize("where", ["first", "last", "middle"])
 def test_infinite_values_of_no_weight(mep, where, n, single):
