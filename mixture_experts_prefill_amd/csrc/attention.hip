@@ -237,8 +237,10 @@ __device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int gro
 // A value that is not finite reaches every row that reads its token, as it is
 // (two of unequal signs make NaN), however small the weight.  The matrix
 // products do not give that: 0 times infinity is NaN, and so is infinity
-// times a weight's two terms of unequal signs.  They run as if all values were
-// finite, and an output that then is not is computed here, from the definition:
+// times a weight's two terms of unequal signs.  And their sums of weights up to
+// 2^8, divided at the end only, may pass fp32 where the values do not.  They run
+// as if neither occurred, and an output that then is not finite is computed
+// here, from the definition:
 //
 //   y = sum_j (w_j / l) v_j over the finite values, or the sum of those that are not
 //
@@ -532,9 +534,9 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
             ls += f * red_l[w][r];
             sum += f * *reinterpret_cast<const f32x4 *>(&red[(w * 16 + r) * D + (col ^ r) * 4]);
         }
+        const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+        sum *= inv;
         if (u.split == 1) {
-            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-            sum *= inv;
             *reinterpret_cast<uint2 *>(out_at(r, col)) = make_uint2(pk_bf16(sum.x, sum.y), pk_bf16(sum.z, sum.w));
         } else {
             *reinterpret_cast<f32x4 *>(a.part + part_at(r) * D + col * 4) = sum;
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
             float *to = a.part + part_at(r) * D + col * 4;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (!q8::finite(to[e])) to[e] = y[i][e] * a.stats[part_at(r)].y;
+                if (!q8::finite(to[e])) to[e] = y[i][e];
         }
     }
 }
@@ -640,7 +642,7 @@ __device__ __forceinline__ void rows_again(const Again &n) {
             for (int e = 0; e < 4; ++e) {
                 if (!wild(i, e)) continue;
                 if (n.slot < 0) out[64 * i + e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
-                else part[i * step + e] = y[i][e] * a.stats[block * 32 + r].y;
+                else part[i * step + e] = y[i][e];
             }
     }
 }
@@ -1037,7 +1039,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     if (!wave_live) return;
     l += __shfl_xor(l, 32, 64);
     f32x4 wild = {0, 0, 0, 0};  // NaN once an output is not finite
-    const float inv = u.split > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -1079,13 +1081,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
 
 // ------------------------------------------------------------------ joining
 
-// Partial outputs are weighted by 2^(m - largest m) and divided by the sum of
-// the sums weighted so, in order.  Bound by the parts' bytes, or by latency.
+// A part is an output of its own, divided by its sum, so that it is finite
+// where the values are.  The whole is the parts weighted by w = l 2^(m - largest
+// m) over the sum of those.  Bound by the parts' bytes, or by latency.
+__device__ __forceinline__ float part_weight(float m, float top) {
+    return m == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+}
 // A weight too small for fp32 is its smallest value and not 0, which would make
 // NaN of a part that is infinite.
-__device__ __forceinline__ float part_weight(float m, float top) {
-    return m == minus_inf() ? 0.0f : fmaxf(__builtin_amdgcn_exp2f(m - top), 0x1p-149f);
-}
+__device__ __forceinline__ float some(float w) { return fmaxf(w, 0x1p-149f); }
 
 // Where the parts of a (row, query head) stand: slots slot0 .. slot0 + split - 1
 // at row `in` of head tile ht; false if it was not cut, or is no sequence's.
@@ -1130,8 +1134,7 @@ template <bool PREFILL, int D, bool WIDE>
 __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
     constexpr int V = D / 64;  // columns a lane
     typedef float vec __attribute__((ext_vector_type(V)));
-    __shared__ vec wave_sum[WIDE ? 3 : 1][64];
-    __shared__ float wave_l[4];
+    __shared__ vec sums[WIDE ? 3 : 1][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, H = a.c.heads, G = a.heads_q / H;
     const int QT = PREFILL ? 1 : (G + kDecodeRows - 1) / kDecodeRows, HT = H * QT;
     if (a.info[0].x == 0) return;
@@ -1156,37 +1159,33 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
         for (int i = lane + 64; i < split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+        float w = mine.y * part_weight(mine.x, top), l = w;
+        for (int i = lane + 64; i < split; i += 64) l += a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top);
+        l = wave_sum(l);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        w *= inv;
         vec sum;
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] = 0.0f;
-        float l = 0.0f;
         auto add = [&](int i, vec v) {
-            const float2 st = i < 64 ? make_float2(__shfl(mine.x, i, 64), __shfl(mine.y, i, 64)) : a.stats[place(i)];
-            const float f = part_weight(st.x, top);
-            l += f * st.y;
-            sum += f * v;
+            sum += some(i < 64 ? __shfl(w, i, 64) : a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top) * inv) * v;
         };
 #pragma unroll
         for (int i = 0; i < FIRST; ++i)
             if (i0 + i < i1) add(i0 + i, part[i]);
         for (int i = i0 + FIRST; i < i1; ++i) add(i, *reinterpret_cast<const vec *>(a.part + place(i) * D + lane * V));
         if (WIDE) {
-            if (wave > 0) wave_sum[WIDE ? wave - 1 : 0][lane] = sum;
-            if (lane == 0) wave_l[wave] = l;
+            if (wave > 0) sums[WIDE ? wave - 1 : 0][lane] = sum;
             __syncthreads();
             if (wave == 0) {
 #pragma unroll
-                for (int w = 1; w < 4; ++w) {
-                    sum += wave_sum[WIDE ? w - 1 : 0][lane];
-                    l += wave_l[w];
-                }
+                for (int w = 1; w < 4; ++w) sum += sums[WIDE ? w - 1 : 0][lane];
             }
         }
         if (!WIDE || wave == 0) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             __bf16 y[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = (__bf16)(sum[j] * inv);
+            for (int j = 0; j < V; ++j) y[j] = (__bf16)sum[j];
             __builtin_memcpy(__builtin_assume_aligned(a.out + p.to * a.ldo + (size_t)hq * D + lane * V, 2 * V), y, 2 * V);
         }
         if (WIDE) __syncthreads();
@@ -1212,27 +1211,31 @@ __global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
         const size_t step = (size_t)H * (a.part_rows / 32), block = ((size_t)slot * H + h) * (a.part_rows / 32) + wave;
         const float2 *stats = a.stats + block * 32 + m;
         const f32x4 *part = reinterpret_cast<const f32x4 *>(a.part) + (block * ND + i) * (4 * 64) + lane;
-        float top = minus_inf();
-        for (int p = 0; p < split; ++p) top = fmaxf(top, stats[p * step * 32].x);
+        float top = minus_inf(), l = 0.0f;
+#pragma unroll 4
+        for (int p = 0; p < split; ++p) {
+            const float2 st = stats[p * step * 32];
+            const float now = fmaxf(top, st.x);
+            l = l * part_weight(top, now) + st.y * part_weight(st.x, now);
+            top = now;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         f32x4 sum[4];
-        float l = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = (f32x4){0, 0, 0, 0};
 #pragma unroll 4
         for (int p = 0; p < split; ++p) {
             const float2 st = stats[p * step * 32];
-            const float f = part_weight(st.x, top);
-            l += f * st.y;
+            const float w = some(st.y * part_weight(st.x, top) * inv);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] += f * part[p * step * (ND * 4 * 64) + j * 64];
+            for (int j = 0; j < 4; ++j) sum[j] += w * part[p * step * (ND * 4 * 64) + j * 64];
         }
         if (x >= rows * G) continue;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t *to = a.out + (size_t)(first + x / G) * a.ldo + (size_t)(h * G + x % G) * D + 32 * i + 4 * hf;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint2 *>(to + 8 * j) =
-                make_uint2(pk_bf16(sum[j].x * inv, sum[j].y * inv), pk_bf16(sum[j].z * inv, sum[j].w * inv));
+                make_uint2(pk_bf16(sum[j].x, sum[j].y), pk_bf16(sum[j].z, sum[j].w));
     }
 }
 

@@ -1,5 +1,6 @@
 """moe_attention_decode and moe_attention_prefill on values at the ends of
-their types: infinities and NaN in values, at any weight.
+their types: infinities and NaN in values, at any weight; finite values whose
+weighted sum passes fp32 before it is divided.
 
 A value that is not finite reaches every row that reads its token, as it is:
 two infinities of unequal signs, or a NaN, make a NaN.  All other columns keep
@@ -16,6 +17,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+MOST = torch.finfo(BF16).max
 
 
 def set_value(b, s, token, column, v, head=0):
@@ -125,3 +127,40 @@ def test_nan_codes(mep, head, single):
     for s, n in enumerate(b.lengths):
         b.cache.section("v").view(torch.uint8)[b.cache.index("v", [b.slots[s][n // 2]])[0, 1, 7]] = 0x7f
     run(mep, b, [1, 70, 20], 6, head ** -0.5, single, (head, single))
+
+
+# ------------------------------------------------------------------ values that are large, and small ones beside them
+
+def with_large_values(mep, lengths, heads, head, dtype):
+    """Columns of the largest values of one sign, of mixed signs, and (bf16) of values of 2^-100 and 2^-120."""
+    b = base.Batch(mep, lengths, heads, head, 32, dtype)
+    for s, n in enumerate(lengths):
+        if n == 0:
+            continue
+        sign = torch.randint(0, 2, (n, heads, head), generator=b.gen).double() * 2 - 1
+        part = torch.rand(n, heads, head, generator=b.gen).double() * 0.5 + 0.5
+        x = sign * part
+        x[:, :, : head // 4] = 1.0
+        x[:, :, head // 4: head // 2] = -part[:, :, head // 4: head // 2]
+        if dtype == BF16:
+            v = (x * MOST).to(BF16)
+            v[:, :, head - 8:head - 4] = (torch.randn(n, heads, 4, generator=b.gen).double() * 2.0 ** -100).to(BF16)
+            v[:, :, head - 4:] = (torch.randn(n, heads, 4, generator=b.gen).double() * 2.0 ** -120).to(BF16)
+            b.cache.write("v", b.slots[s], v)
+        else:
+            b.cache.write("v", b.slots[s], (x * 240).to(E4M3), torch.full((n, heads), 247, dtype=torch.uint8))
+    return b
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("head", [64, 128, 256])
+def test_large_values(mep, head, single, dtype):
+    b = with_large_values(mep, [1, 2, 33, 300, 0, 5000], 2, head, dtype)
+    run(mep, b, [1, 2, 33, 150, 0, 40], 6, head ** -0.5, single, (head, single, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_large_values_joined_by_tiles(mep, dtype):
+    b = with_large_values(mep, [900, 1300], 1, 128, dtype)
+    run(mep, b, [400, 260], 8, 128 ** -0.5, False, dtype)
