@@ -238,15 +238,17 @@ __device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int gro
 // (two of unequal signs make NaN), however small the weight.  The matrix
 // products do not give that: 0 times infinity is NaN, and so is infinity
 // times a weight's two terms of unequal signs.  And their sums of weights up to
-// 2^8, divided at the end only, may pass fp32 where the values do not.  They run
-// as if neither occurred, and an output that then is not finite is computed
-// here, from the definition:
+// 2^8, divided at the end only, may pass fp32 where the values do not, as may
+// the largest score times the scale (weights are then 0 or infinite, and their
+// sum too).  They run as if none of this occurred, and an output that then is
+// not finite is computed here, from the definition:
 //
 //   y = sum_j (w_j / l) v_j over the finite values, or the sum of those that are not
 //
 // 16 lanes a row, a token each: tokens j0 .. j1 - 1 of the sequence whose pages
 // are `pages`, key head h, query row q.  m and l are the row's maximum and sum;
-// columns 4 (lane % 16 + 16 i) .. + 3 are y[i].  No step of the fast path: an
+// columns 4 (lane % 16 + 16 i) .. + 3 are y[i].  Scores are scaled after the
+// largest is taken off.  No step of the fast path: an
 // output takes as long as the row's products without the matrix core, three times.
 template <int CT, int D>
 __device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const int32_t *pages, int h, const uint16_t *q,
@@ -534,13 +536,13 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
             ls += f * red_l[w][r];
             sum += f * *reinterpret_cast<const f32x4 *>(&red[(w * 16 + r) * D + (col ^ r) * 4]);
         }
-        const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+        const float inv = top == minus_inf() ? 0.0f : 1.0f / ls;
         sum *= inv;
         if (u.split == 1) {
             *reinterpret_cast<uint2 *>(out_at(r, col)) = make_uint2(pk_bf16(sum.x, sum.y), pk_bf16(sum.z, sum.w));
         } else {
             *reinterpret_cast<f32x4 *>(a.part + part_at(r) * D + col * 4) = sum;
-            if (col == 0) a.stats[part_at(r)] = make_float2(top * cs, ls);
+            if (col == 0) a.stats[part_at(r)] = make_float2(top, ls);
         }
         wild = wild || !(q8::finite(sum.x) && q8::finite(sum.y) && q8::finite(sum.z) && q8::finite(sum.w));
     }
@@ -567,6 +569,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (!q8::finite(to[e])) to[e] = y[i][e];
+            if (col == 0) a.stats[part_at(r)] = make_float2(m_r, l_r);
         }
     }
 }
@@ -644,6 +647,7 @@ __device__ __forceinline__ void rows_again(const Again &n) {
                 if (n.slot < 0) out[64 * i + e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
                 else part[i * step + e] = y[i][e];
             }
+        if (n.slot >= 0 && mine == 0) a.stats[block * 32 + r] = make_float2(m, l);
     }
 }
 
@@ -1039,7 +1043,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     if (!wave_live) return;
     l += __shfl_xor(l, 32, 64);
     f32x4 wild = {0, 0, 0, 0};  // NaN once an output is not finite
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = mx == minus_inf() ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -1058,7 +1062,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
                     *reinterpret_cast<uint2 *>(a.out + at + 32 * i + 2 * j + 4 * hf) =
                         make_uint2(pk_bf16(o[i][j], o[i][j + 1]), pk_bf16(o[i][j + 2], o[i][j + 3]));
     } else if (a.by_tile) {  // as the registers are, which is how the joining launch reads them
-        if (hf == 0) a.stats[block * 32 + m] = make_float2(mx * cs, l);
+        if (hf == 0) a.stats[block * 32 + m] = make_float2(mx, l);
         f32x4 *part = reinterpret_cast<f32x4 *>(a.part) + block * (ND * 4 * 64) + lane;
 #pragma unroll
         for (int i = 0; i < ND; ++i)
@@ -1067,7 +1071,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
                 part[(i * 4 + j) * 64] = (f32x4){o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
     } else if (live) {
         const size_t at = ((size_t)u.slot * H + h) * a.part_rows + wave * 32 + m;
-        if (hf == 0) a.stats[at] = make_float2(mx * cs, l);
+        if (hf == 0) a.stats[at] = make_float2(mx, l);
 #pragma unroll
         for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -1082,10 +1086,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
 // ------------------------------------------------------------------ joining
 
 // A part is an output of its own, divided by its sum, so that it is finite
-// where the values are.  The whole is the parts weighted by w = l 2^(m - largest
-// m) over the sum of those.  Bound by the parts' bytes, or by latency.
-__device__ __forceinline__ float part_weight(float m, float top) {
-    return m == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+// where the values are.  The whole is the parts weighted by w = l exp(scale (m -
+// largest m)) over the sum of those.  Bound by the parts' bytes, or by latency.
+__device__ __forceinline__ float part_weight(float m, float top, float cs) {
+    return m == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f((m - top) * cs);
 }
 // A weight too small for fp32 is its smallest value and not 0, which would make
 // NaN of a part that is infinite.
@@ -1137,6 +1141,7 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
     __shared__ vec sums[WIDE ? 3 : 1][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, H = a.c.heads, G = a.heads_q / H;
     const int QT = PREFILL ? 1 : (G + kDecodeRows - 1) / kDecodeRows, HT = H * QT;
+    const float cs = a.scale * kLog2e;
     if (a.info[0].x == 0) return;
     const int rows = PREFILL ? min(max(a.starts[a.n], 0), a.t) : a.n;
     const int step = WIDE ? gridDim.x : gridDim.x * 4;
@@ -1159,8 +1164,8 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
         for (int i = lane + 64; i < split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-        float w = mine.y * part_weight(mine.x, top), l = w;
-        for (int i = lane + 64; i < split; i += 64) l += a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top);
+        float w = mine.y * part_weight(mine.x, top, cs), l = w;
+        for (int i = lane + 64; i < split; i += 64) l += a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top, cs);
         l = wave_sum(l);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         w *= inv;
@@ -1168,7 +1173,7 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] = 0.0f;
         auto add = [&](int i, vec v) {
-            sum += some(i < 64 ? __shfl(w, i, 64) : a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top) * inv) * v;
+            sum += some(i < 64 ? __shfl(w, i, 64) : a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top, cs) * inv) * v;
         };
 #pragma unroll
         for (int i = 0; i < FIRST; ++i)
@@ -1199,6 +1204,7 @@ __global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
     constexpr int ND = D / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 31, hf = lane >> 5;
     const int H = a.c.heads, G = a.heads_q / H;
+    const float cs = a.scale * kLog2e;
     const int items = min(a.info[0].x, a.slots) * H * ND;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int i = item % ND, h = item / ND % H, slot = item / ND / H;
@@ -1216,7 +1222,7 @@ __global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
         for (int p = 0; p < split; ++p) {
             const float2 st = stats[p * step * 32];
             const float now = fmaxf(top, st.x);
-            l = l * part_weight(top, now) + st.y * part_weight(st.x, now);
+            l = l * part_weight(top, now, cs) + st.y * part_weight(st.x, now, cs);
             top = now;
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1226,7 +1232,7 @@ __global__ void __launch_bounds__(256) k_join_tiles(AttentionArgs a) {
 #pragma unroll 4
         for (int p = 0; p < split; ++p) {
             const float2 st = stats[p * step * 32];
-            const float w = some(st.y * part_weight(st.x, top) * inv);
+            const float w = some(st.y * part_weight(st.x, top, cs) * inv);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] += w * part[p * step * (ND * 4 * 64) + j * 64];
         }

@@ -61,8 +61,8 @@ moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t
         return fail(MOE_ERR_INVALID, "%s: t = %d rows of n = %d sequences need starts", who, t, n);
     if (!q || !cache || !table || !length || !out || !workspace || (prefill && !starts))
         return fail(MOE_ERR_INVALID, "%s: null pointer", who);
-    if (!(scale >= 1.17549435e-38f) || scale == __builtin_inff())
-        return fail(MOE_ERR_INVALID, "%s: scale must be finite and at least 2^-126", who);
+    if (!(scale >= 0x1p-126f) || scale > 0x1p127f)  // times log2 e it is still finite
+        return fail(MOE_ERR_INVALID, "%s: scale must be from 2^-126 to 2^127", who);
     const int64_t width = (int64_t)heads_q * L->head;
     if (moe_status st = check_rows16(q, ldq, width, MOE_BF16, who, "q")) return st;
     if (moe_status st = check_rows16(out, ldo, width, MOE_BF16, who, "out")) return st;

@@ -58,8 +58,9 @@ struct AttentionArgs {
     bool by_tile;
     float scale;
     bool prefill;
-    // workspace: what the joining launch has to know; partial outputs of
-    // [slot][head tile] part_rows rows, and their (maximum, sum) pairs
+    // workspace: what the joining launch has to know; outputs of the parts,
+    // [slot][head tile] part_rows rows, and the largest score and the sum of
+    // weights relative to it that each row of them has
     int4 *info;
     float *part;
     float2 *stats;

@@ -1,6 +1,6 @@
 """moe_attention_decode and moe_attention_prefill on values at the ends of
 their types: infinities and NaN in values, at any weight; finite values whose
-weighted sum passes fp32 before it is divided.
+weighted sum passes fp32 before it is divided; scores beyond fp32.
 
 A value that is not finite reaches every row that reads its token, as it is:
 two infinities of unequal signs, or a NaN, make a NaN.  All other columns keep
@@ -164,3 +164,30 @@ def test_large_values(mep, head, single, dtype):
 def test_large_values_joined_by_tiles(mep, dtype):
     b = with_large_values(mep, [900, 1300], 1, 128, dtype)
     run(mep, b, [400, 260], 8, 128 ** -0.5, False, dtype)
+
+
+# ------------------------------------------------------------------ scores
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** 125])
+@pytest.mark.parametrize("n", [1, 50, 700, 5000])
+def test_scores_beyond_fp32(mep, n, scale, single):
+    """Products q.k of up to 6 that the scale takes out of fp32: the largest one's token is all there is."""
+    head, hq, rows = 64, 2, 1 if single else min(n, 30)
+    b = base.Batch(mep, [n], 1, head, 16, BF16)
+    k = torch.zeros(n, 1, head)
+    k[:, 0, 0] = torch.randint(-8, 3, (n,), generator=b.gen).float() * 0.5
+    best = (n - rows) // 2
+    k[best, 0, 0] = 3.0
+    b.cache.write("k", b.slots[0], k.to(BF16))
+    q = torch.zeros(rows, hq * head, dtype=BF16)
+    q[:, 0], q[:, head] = 1.0, 2.0
+    cache, table, length = b.on_gpu()
+    out = torch.empty(rows, hq * head, dtype=BF16, device="cuda")
+    ws = base.workspace(mep, rows, 1, hq, b.layout)
+    if single:
+        mep.moe_attention_decode(q.cuda(), b.layout, cache, table, length, scale, out, ws)
+    else:
+        mep.moe_attention_prefill(q.cuda(), base.ints([0, rows]).cuda(), b.layout, cache, table, length, scale, out, ws)
+    want = b.values(0)[1][best].view(1, head).expand(rows * hq, head)
+    assert torch.equal(out.double().cpu().view(rows * hq, head), want)
