@@ -666,8 +666,10 @@ moe_status moe_kv_layout_make(int32_t pages, int32_t page, int32_t heads, int32_
  *                           table names a page that the cache lacks, or the row is past starts[n]
  *   lacking        [1]      rows asked for (all grow[s] > 0) that have no slot, at most 2^31 - 1: 0 in a good step
  * A sequence whose rows do not all have pages ends behind the last one that
- * does (length_out).  Where length and free_n are not written in place, the
- * step can then be planned again with fewer rows.  A length outside 0 ..
+ * does (length_out): its rows are then not its last tokens, and attention has
+ * to be told where they start (moe_attention_*_step).  Where length and free_n
+ * are not written in place, the step can be planned again with fewer rows, as
+ * it can be after moe_kv_plan_step.  A length outside 0 ..
  * max_pages * page counts as the nearest of these.  The kernel reads and
  * writes nothing out of bounds whatever the integers are.
  * Requires 1 <= n <= MOE_MAX_ROWS, 1 <= t <= MOE_MAX_ROWS, max_pages >= 1,
@@ -678,6 +680,17 @@ moe_status moe_kv_plan(const int32_t *length, const int32_t *grow, int32_t n, in
                        int32_t *table, int32_t max_pages, int64_t ldt, int32_t *free_pages, const int32_t *free_n,
                        int32_t *length_out, int32_t *free_n_out, int32_t *starts, int32_t *positions,
                        int32_t *slots, int32_t *lacking, void *stream);
+
+/*
+ * The same with length and free_n in place, and a way back.  before [n + 1]
+ * becomes the lengths and *free_n as they are before the step, or with again
+ * != 0 is read as those: the step then takes the place of the one planned last
+ * (fewer rows where that one lacked pages).  before must not overlap anything.
+ */
+moe_status moe_kv_plan_step(int32_t *length, const int32_t *grow, int32_t n, int32_t t, const moe_kv_layout *L,
+                            int32_t *table, int32_t max_pages, int64_t ldt, int32_t *free_pages, int32_t *free_n,
+                            int32_t *before, int32_t again, int32_t *starts, int32_t *positions, int32_t *slots,
+                            int32_t *lacking, void *stream);
 
 /*
  * Rows of new keys and values into the cache, rotated by their positions,
@@ -769,6 +782,26 @@ moe_status moe_attention_prefill(const uint16_t *q, int64_t ldq, const int32_t *
                                  int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
                                  int32_t max_pages, int64_t ldt, const int32_t *length, float scale, uint16_t *out,
                                  int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same for a step that may lack pages: before [n] (held in 0 .. max_pages *
+ * page) says how many tokens each sequence had, so that the positions of its
+ * rows do not rest on its length.  The row i of sequence s (decode: its last
+ * row) sits at position before[s] + i and reads, in prefill, the tokens up to
+ * it, in decode all length[s]; a row at length[s] or after has no slot and is
+ * 0.  Where every row has its slot, the result is bitwise that of the calls
+ * above.  before must not overlap out or the workspace.
+ */
+moe_status moe_attention_decode_step(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                     int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                     int32_t max_pages, int64_t ldt, const int32_t *length, const int32_t *before,
+                                     float scale, uint16_t *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+moe_status moe_attention_prefill_step(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                      int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                      int32_t max_pages, int64_t ldt, const int32_t *length, const int32_t *before,
+                                      float scale, uint16_t *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                      void *stream);
 
 #ifdef __cplusplus
 }

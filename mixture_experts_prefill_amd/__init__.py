@@ -77,7 +77,8 @@ EXPORTS = ["moe_last_error", "moe_layout_make", "moe_workspace_bytes", "moe_rout
            "moe_block_from_residual", "moe_chunk_stats_fill", "moe_debug_read_probe",
            "moe_debug_schedule", "moe_debug_xcc_map", "moe_debug_tile_wait", "moe_matrix_layout_make",
            "moe_linear", "moe_linear_gated", "moe_residual_norm", "moe_kv_layout_make", "moe_kv_plan",
-           "moe_kv_append", "moe_attention_workspace_bytes", "moe_attention_decode", "moe_attention_prefill"]
+           "moe_kv_append", "moe_attention_workspace_bytes", "moe_attention_decode", "moe_attention_prefill",
+           "moe_kv_plan_step", "moe_attention_decode_step", "moe_attention_prefill_step"]
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 PHASES = ["router", "topk", "csr", "shared_gateup", "shared_down", "schedule", "gateup", "down", "combine", "norm",
           "experts", "linear", "kv", "attention"]  # MOE_PHASE_* in order; moe_profile_end fills one entry each
@@ -134,11 +135,14 @@ def lib():
     KP = ctypes.POINTER(moe_kv_layout)
     L.moe_kv_layout_make.argtypes = [I, I, I, I, I, KP]
     L.moe_kv_plan.argtypes = [P, P, I, I, KP, P, I, Q, P, P, P, P, P, P, P, P, P]
+    L.moe_kv_plan_step.argtypes = [P, P, I, I, KP, P, I, Q, P, P, P, I, P, P, P, P, P]
     L.moe_kv_append.argtypes = [P, Q, P, Q, I, I, KP, P, P, P, P, I, I, P, Q, I, P, Q, P]
     L.moe_attention_workspace_bytes.argtypes = [I, I, I, KP]
     L.moe_attention_workspace_bytes.restype = Z
     L.moe_attention_decode.argtypes = [P, Q, P, I, I, I, KP, P, P, I, Q, P, ctypes.c_float, P, Q, P, Z, P]
     L.moe_attention_prefill.argtypes = [P, Q, P, I, I, I, KP, P, P, I, Q, P, ctypes.c_float, P, Q, P, Z, P]
+    for f in (L.moe_attention_decode_step, L.moe_attention_prefill_step):
+        f.argtypes = [P, Q, P, I, I, I, KP, P, P, I, Q, P, P, ctypes.c_float, P, Q, P, Z, P]
     L.moe_ring_plan_debug.argtypes = [P, P, I, I, I, P, P, P]
     L.moe_profile_begin.argtypes = [ctypes.c_uint32]
     L.moe_profile_begin.restype = None
@@ -150,7 +154,8 @@ def lib():
               "moe_ring_get_stats", "moe_prefill_experts", "moe_prefill_fused", "moe_block", "moe_block_noalloc", "moe_inject_norm", "moe_block_next_norm",
               "moe_residency", "moe_lookahead", "moe_block_from_residual", "moe_chunk_stats_fill",
               "moe_matrix_layout_make", "moe_linear", "moe_linear_gated", "moe_residual_norm", "moe_kv_layout_make",
-              "moe_kv_plan", "moe_kv_append", "moe_attention_decode", "moe_attention_prefill"):
+              "moe_kv_plan", "moe_kv_append", "moe_attention_decode", "moe_attention_prefill", "moe_kv_plan_step",
+              "moe_attention_decode_step", "moe_attention_prefill_step"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
@@ -659,6 +664,23 @@ def moe_kv_plan(length: torch.Tensor, grow: torch.Tensor, layout: moe_kv_layout,
              _ints(positions, t, dev, "positions"), _ints(slots, t, dev, "slots"), _ints(lacking, 1, dev, "lacking"))
 
 
+def moe_kv_plan_step(length: torch.Tensor, grow: torch.Tensor, layout: moe_kv_layout, table: torch.Tensor,
+                     free_pages: torch.Tensor, free_n: torch.Tensor, before: torch.Tensor, starts: torch.Tensor,
+                     positions: torch.Tensor, slots: torch.Tensor, lacking: torch.Tensor, again: bool = False,
+                     stream=None) -> None:
+    """moe_kv_plan with length and free_n in place, which are kept as they were in before [n + 1]; again: the step is
+    planned another time, from there."""
+    dev, n, t = length.get_device(), length.numel(), positions.numel()
+    if dev < 0:
+        raise ValueError("tensors passed to libmoe must be on one GPU")
+    tp, width, ldt = _table_args(table, n, dev)
+    _call_on(dev, stream, (_lib or lib()).moe_kv_plan_step, _ints(length, n, dev, "length"), _ints(grow, n, dev, "grow"), n, t,
+             ctypes.byref(layout), tp, width, ldt, _ints(free_pages, layout.pages, dev, "free_pages"),
+             _ints(free_n, 1, dev, "free_n"), _ints(before, n + 1, dev, "before"), int(again),
+             _ints(starts, n + 1, dev, "starts"), _ints(positions, t, dev, "positions"), _ints(slots, t, dev, "slots"),
+             _ints(lacking, 1, dev, "lacking"))
+
+
 def moe_kv_append(k: torch.Tensor, v: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor, slots: torch.Tensor,
                   positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -706,28 +728,39 @@ def _attention_args(q, layout, cache, table, n, length, out, workspace):
 
 def moe_attention_decode(q: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor, table: torch.Tensor,
                          length: torch.Tensor, scale: float, out: torch.Tensor, workspace: torch.Tensor,
-                         starts: Optional[torch.Tensor] = None, stream=None) -> None:
+                         starts: Optional[torch.Tensor] = None, stream=None, before: Optional[torch.Tensor] = None) -> None:
     """out [t, heads_q * head] = attention of one row a sequence, q [t, heads_q * head] bfloat16, over its first
     length[s] tokens: row s, or with starts [n + 1] the last of rows starts[s] .. starts[s + 1] - 1, if any;
-    workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes."""
+    workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes.  before [n]: tokens before the step, of which
+    a row without a slot is told, and is 0."""
     n = length.numel()
     dev, t, hq, qp, ldq, cp, tp, width, ldt, lp, op, ldo, wp, wn = _attention_args(
         q, layout, cache, table, n, length, out, workspace)
-    _call_on(dev, stream, (_lib or lib()).moe_attention_decode, qp, ldq,
-             None if starts is None else _ints(starts, n + 1, dev, "starts"), t, n, hq, ctypes.byref(layout), cp, tp, width,
-             ldt, lp, scale, op, ldo, wp, wn)
+    sp = None if starts is None else _ints(starts, n + 1, dev, "starts")
+    if before is None:
+        _call_on(dev, stream, (_lib or lib()).moe_attention_decode, qp, ldq, sp, t, n, hq, ctypes.byref(layout), cp, tp, width,
+                 ldt, lp, scale, op, ldo, wp, wn)
+    else:
+        _call_on(dev, stream, (_lib or lib()).moe_attention_decode_step, qp, ldq, sp, t, n, hq, ctypes.byref(layout), cp, tp,
+                 width, ldt, lp, _ints(before, n, dev, "before"), scale, op, ldo, wp, wn)
 
 
 def moe_attention_prefill(q: torch.Tensor, starts: torch.Tensor, layout: moe_kv_layout, cache: torch.Tensor,
                           table: torch.Tensor, length: torch.Tensor, scale: float, out: torch.Tensor,
-                          workspace: torch.Tensor, stream=None) -> None:
+                          workspace: torch.Tensor, stream=None, before: Optional[torch.Tensor] = None) -> None:
     """Causal attention of the packed rows q [t, heads_q * head], rows starts[s] .. starts[s + 1] - 1 being the last
-    of the length[s] tokens of sequence s; workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes."""
+    of the length[s] tokens of sequence s; workspace of moe_attention_workspace_bytes(t, n, heads_q, layout) bytes.
+    before [n]: they are instead the tokens from position before[s] on, and 0 from length[s] on (rows without a slot)."""
     n = length.numel()
     dev, t, hq, qp, ldq, cp, tp, width, ldt, lp, op, ldo, wp, wn = _attention_args(
         q, layout, cache, table, n, length, out, workspace)
-    _call_on(dev, stream, (_lib or lib()).moe_attention_prefill, qp, ldq, _ints(starts, n + 1, dev, "starts"), t, n, hq,
-             ctypes.byref(layout), cp, tp, width, ldt, lp, scale, op, ldo, wp, wn)
+    sp = _ints(starts, n + 1, dev, "starts")
+    if before is None:
+        _call_on(dev, stream, (_lib or lib()).moe_attention_prefill, qp, ldq, sp, t, n, hq, ctypes.byref(layout), cp, tp, width,
+                 ldt, lp, scale, op, ldo, wp, wn)
+    else:
+        _call_on(dev, stream, (_lib or lib()).moe_attention_prefill_step, qp, ldq, sp, t, n, hq, ctypes.byref(layout), cp, tp,
+                 width, ldt, lp, _ints(before, n, dev, "before"), scale, op, ldo, wp, wn)
 
 
 def moe_ring_plan_debug(offsets, resident, n_slots: int = 64, group: int = 8):

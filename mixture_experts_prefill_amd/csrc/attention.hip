@@ -90,6 +90,7 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) { return __uint_as_
 // A unit of work: a tile of a sequence over a run of its tokens.
 struct Unit {
     int s, len, rows, first;  // the sequence, its tokens, its rows and the first of them
+    int before;               // (prefill) the first row's position
     int tile, split, part;    // part of the `split` parts of the tile's tokens
     int slot;                 // where its partial result goes (split > 1)
     int cuts;                 // partial results of the head in all
@@ -97,7 +98,7 @@ struct Unit {
 
 // One sequence as the units see it.
 struct Seq {
-    int len, rows, first, tiles;
+    int len, rows, first, before, tiles;
     int least;  // tokens of a part at the least
 };
 template <bool PREFILL>
@@ -115,6 +116,8 @@ __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) 
         if (!PREFILL) q.first = end - 1;
         if (PREFILL && q.tiles > 1) q.least = max(q.least, 2 * q.rows >= q.len ? a.least_whole : kLeastTiles);
     }
+    q.before = a.before ? min(max(a.before[s], 0), a.max_tokens) : q.len - q.rows;
+    if (!PREFILL && q.before + q.rows > q.len) q.len = 0;  // the row has no slot
     return q;
 }
 // Tokens that a part has, for tiles of `work` tokens in all and heads (head tiles) of them.
@@ -139,7 +142,7 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
     const int tid = threadIdx.x, lane = tid & 63;
     u.cuts = 0;
     if (SMALL) {
-        Seq q = {0, 0, 0, 0, 1};
+        Seq q = {0, 0, 0, 0, 0, 1};
         if (lane < a.n) q = seq_of<PREFILL>(a, lane, group);
         const float work = wave_sum((float)q.tiles * q.len);
         const int n = lane < a.n ? splits(q, part_tokens<PREFILL>(work, heads)) : 0;
@@ -150,7 +153,7 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
         const int s = __builtin_ctzll(past);
         auto get = [&](int x) { return __builtin_amdgcn_readlane(x, s); };
         const int at = v - get(ue - units), n_s = get(n), tiles = get(q.tiles);
-        u = Unit{s, get(q.len), get(q.rows), get(q.first), tiles - 1 - at / n_s, n_s, at % n_s, get(pe - parts),
+        u = Unit{s, get(q.len), get(q.rows), get(q.first), get(q.before), tiles - 1 - at / n_s, n_s, at % n_s, get(pe - parts),
                  __builtin_amdgcn_readlane(pe, 63)};
     } else {
         __shared__ float wave_work[4];
@@ -193,7 +196,7 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
                 const int n = splits(q, tokens);
                 if (v < ub + q.tiles * n) {
                     const int at = v - ub;
-                    found = Unit{s, q.len, q.rows, q.first, q.tiles - 1 - at / n, n, at % n, pb, 0};
+                    found = Unit{s, q.len, q.rows, q.first, q.before, q.tiles - 1 - at / n, n, at % n, pb, 0};
                     break;
                 }
                 ub += q.tiles * n;
@@ -600,8 +603,8 @@ __device__ __forceinline__ bool not_finite(u32x4 w) {
 
 // What rows that are computed again need of their unit.
 struct Again {
-    int s, first, slot;               // the sequence, its first row, the unit's partial result (-1: none)
-    int x0, pairs, before, j0, j1;    // the tile's first pair, the sequence's pairs, its tokens before its rows, the unit's tokens
+    int s, len, first, slot;          // the sequence, its tokens, its first row, the unit's partial result (-1: none)
+    int x0, pairs, before, j0, j1;    // the tile's first pair, the sequence's pairs, its first row's position, the unit's tokens
 };
 // The outputs of the wave's 32 pairs that are not finite, by definition, in
 // the place of what k_prefill has written.  All that is known of the launch is read
@@ -637,8 +640,9 @@ __device__ __forceinline__ void rows_again(const Again &n) {
         if (!(__ballot(any) >> (lane & 48) & 0xffff)) continue;
         float m, l;
         f32x4 y[D / 64];
+        const int pos = n.before + token;
         row_by_definition<CT, D>(a, pages, h, a.q + (size_t)(n.first + token) * a.ldq + (size_t)hq * D, n.j0,
-                                 min(n.j1, n.before + token + 1), cs, m, l, y);
+                                 pos < n.len ? min(n.j1, pos + 1) : n.j0, cs, m, l, y);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
@@ -680,17 +684,19 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(tile_lds));
 
     // the lane's rows: pair x of the sequence, token x / G, query head x % G; their positions
-    const int pairs = u.rows * G, x0 = u.tile * kPrefillRows, xw = x0 + wave * 32, before = u.len - u.rows;
+    const int pairs = u.rows * G, x0 = u.tile * kPrefillRows, xw = x0 + wave * 32, before = u.before;
     const bool wave_live = xw < pairs;
-    const int wave_min = before + xw / G, wave_max = before + min(xw + 31, pairs - 1) / G;
-    const int tile_min = before + x0 / G, tile_end = max(before + min(x0 + kPrefillRows - 1, pairs - 1) / G + 1, 0);
+    // (rows at u.len and after have no slot: they read nothing, like rows before the first token)
+    const int wave_max = before + min(xw + 31, pairs - 1) / G, wave_min = wave_max < u.len ? before + xw / G : -1;
+    const int tile_max = before + min(x0 + kPrefillRows - 1, pairs - 1) / G, tile_end = min(max(tile_max + 1, 0), u.len);
+    const int tile_min = tile_max < u.len ? before + x0 / G : -1;
     const int tiles = (tile_end + TK - 1) / TK, each = (tiles + u.split - 1) / u.split;
     const int t0 = u.part * each, t1 = min(t0 + each, tiles);
     const int x = xw + m, token = x / G;
     const bool live = x < pairs;
     __shared__ Again again;
-    if (tid == 0) again = Again{u.s, u.first, u.split > 1 ? u.slot : -1, x0, pairs, before, t0 * TK, min(t1 * TK, u.len)};
-    const int pos = live ? before + token : 1 << 30;
+    if (tid == 0) again = Again{u.s, u.len, u.first, u.split > 1 ? u.slot : -1, x0, pairs, before, t0 * TK, min(t1 * TK, u.len)};
+    const int pos = !live ? 1 << 30 : before + token < u.len ? before + token : -1;
     bf16x8 qf[NKS];
     {
         const uint16_t *q = a.q + (live ? (size_t)(u.first + token) * a.ldq + (size_t)(h * G + x % G) * D : 0);

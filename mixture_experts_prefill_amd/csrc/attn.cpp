@@ -50,8 +50,8 @@ moe_status check_table(const moe_kv_layout *L, int n, int max_pages, int64_t ldt
 
 moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t *starts, int t, int n, int heads_q,
                      const moe_kv_layout *L, const void *cache, const int32_t *table, int max_pages, int64_t ldt,
-                     const int32_t *length, float scale, uint16_t *out, int64_t ldo, void *workspace,
-                     size_t workspace_bytes, hipStream_t stream, const char *who) {
+                     const int32_t *length, const int32_t *before, float scale, uint16_t *out, int64_t ldo,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream, const char *who) {
     if (moe_status st = check_t(t, who)) return st;
     if (!layout_ok(L)) return fail(MOE_ERR_INVALID, "%s: layout not made by moe_kv_layout_make", who);
     if (moe_status st = check_table(L, n, max_pages, ldt, who)) return st;
@@ -66,14 +66,15 @@ moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t
     const int64_t width = (int64_t)heads_q * L->head;
     if (moe_status st = check_rows16(q, ldq, width, MOE_BF16, who, "q")) return st;
     if (moe_status st = check_rows16(out, ldo, width, MOE_BF16, who, "out")) return st;
-    if (!aligned(cache, 16) || !aligned(workspace, 16) || !int_aligned({table, length, starts}))
+    if (!aligned(cache, 16) || !aligned(workspace, 16) || !int_aligned({table, length, starts, before}))
         return fail(MOE_ERR_INVALID, "%s: cache and workspace must be 16-byte aligned, integers 4-byte", who);
     const AttentionPlan p = attention_plan(prefill, t, n, heads_q, L->heads, L->head);
     if (workspace_bytes < p.total)
         return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, p.total);
     const Rows ro = rows(out, width * 2, ldo * 2), ws = rows(workspace, p.total, 0);
-    const Rows in[5] = {rows(q, width * 2, ldq * 2), rows(cache, L->bytes, 0),
-                        ints(table, (size_t)(n - 1) * ldt + max_pages), ints(length, n), ints(starts, (size_t)n + 1)};
+    const Rows in[6] = {rows(q, width * 2, ldq * 2), rows(cache, L->bytes, 0),
+                        ints(table, (size_t)(n - 1) * ldt + max_pages), ints(length, n), ints(starts, (size_t)n + 1),
+                        ints(before, n)};
     if (overlap(ro, ws, t)) return fail(MOE_ERR_INVALID, "%s: out must not overlap the workspace", who);
     for (const Rows &i : in)
         if (overlap(ro, i, t) || overlap(ws, i, t))
@@ -86,6 +87,7 @@ moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t
     a.table = table;
     a.length = length;
     a.starts = starts;
+    a.before = before;
     a.ldq = ldq;
     a.ldo = ldo;
     a.ldt = ldt;
@@ -103,6 +105,40 @@ moe_status attention(bool prefill, const uint16_t *q, int64_t ldq, const int32_t
     a.slots = p.slots;
     hipError_t e = launch_attention(a, stream);
     if (e != hipSuccess) return hip_fail(e, who);
+    return MOE_OK;
+}
+
+moe_status kv_plan(const int32_t *length, const int32_t *grow, int32_t n, int32_t t, const moe_kv_layout *L,
+                   int32_t *table, int32_t max_pages, int64_t ldt, int32_t *free_pages, const int32_t *free_n,
+                   int32_t *length_out, int32_t *free_n_out, int32_t *keep, int32_t *starts, int32_t *positions,
+                   int32_t *slots, int32_t *lacking, hipStream_t stream, const char *who) {
+    const size_t N = n;
+    const Rows in[3] = {ints(length, N), ints(grow, N), ints(free_n, 1)};
+    const Rows to[8] = {ints(length_out, N), ints(free_n_out, 1), ints(table, (N - 1) * ldt + max_pages),
+                        ints(free_pages, L->pages), ints(starts, N + 1), ints(positions, t), ints(slots, t),
+                        ints(lacking, 1)};
+    for (int i = 0; i < 8; ++i) {
+        for (int j = 0; j < 3; ++j) {
+            const bool same = (i == 0 && j == 0 && length_out == length) || (i == 1 && j == 2 && free_n_out == free_n);
+            if (!same && overlap(to[i], in[j], 1)) return fail(MOE_ERR_INVALID, "%s: an output overlaps an input", who);
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[i], to[j], 1)) return fail(MOE_ERR_INVALID, "%s: two outputs overlap", who);
+    }
+    const KvPlanArgs a{length, grow, free_n, table, free_pages, length_out, free_n_out, starts, positions, slots, lacking,
+                       keep, ldt, n, t, L->pages, __builtin_ctz(L->page), max_pages};
+    hipError_t e = launch_kv_plan(a, stream);
+    if (e != hipSuccess) return hip_fail(e, who);
+    return MOE_OK;
+}
+
+moe_status check_plan(const moe_kv_layout *L, int n, int t, int max_pages, int64_t ldt, bool pointers, bool alignment,
+                      const char *who) {
+    if (moe_status st = check_t(t, who)) return st;
+    if (!layout_ok(L)) return fail(MOE_ERR_INVALID, "%s: layout not made by moe_kv_layout_make", who);
+    if (moe_status st = check_table(L, n, max_pages, ldt, who)) return st;
+    if (!pointers) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
+    if (!alignment) return fail(MOE_ERR_INVALID, "%s: integers must be 4-byte aligned", who);
     return MOE_OK;
 }
 
@@ -150,32 +186,37 @@ moe_status moe_kv_plan(const int32_t *length, const int32_t *grow, int32_t n, in
                        int32_t *length_out, int32_t *free_n_out, int32_t *starts, int32_t *positions,
                        int32_t *slots, int32_t *lacking, void *stream) {
     const char *who = "kv_plan";
-    if (moe_status st = check_t(t, who)) return st;
-    if (!layout_ok(L)) return fail(MOE_ERR_INVALID, "%s: layout not made by moe_kv_layout_make", who);
-    if (moe_status st = check_table(L, n, max_pages, ldt, who)) return st;
-    if (!length || !grow || !table || !free_pages || !free_n || !length_out || !free_n_out || !starts || !positions ||
-        !slots || !lacking)
-        return fail(MOE_ERR_INVALID, "%s: null pointer", who);
-    if (!int_aligned({length, grow, table, free_pages, free_n, length_out, free_n_out, starts, positions, slots, lacking}))
-        return fail(MOE_ERR_INVALID, "%s: integers must be 4-byte aligned", who);
-    const size_t N = n;
-    const Rows in[3] = {ints(length, N), ints(grow, N), ints(free_n, 1)};
-    const Rows to[8] = {ints(length_out, N), ints(free_n_out, 1), ints(table, (N - 1) * ldt + max_pages),
-                        ints(free_pages, L->pages), ints(starts, N + 1), ints(positions, t), ints(slots, t),
-                        ints(lacking, 1)};
-    for (int i = 0; i < 8; ++i) {
-        for (int j = 0; j < 3; ++j) {
-            const bool same = (i == 0 && j == 0 && length_out == length) || (i == 1 && j == 2 && free_n_out == free_n);
-            if (!same && overlap(to[i], in[j], 1)) return fail(MOE_ERR_INVALID, "%s: an output overlaps an input", who);
-        }
-        for (int j = 0; j < i; ++j)
-            if (overlap(to[i], to[j], 1)) return fail(MOE_ERR_INVALID, "%s: two outputs overlap", who);
-    }
-    const KvPlanArgs a{length, grow, free_n, table, free_pages, length_out, free_n_out, starts, positions, slots, lacking,
-                       ldt, n, t, L->pages, __builtin_ctz(L->page), max_pages};
-    hipError_t e = launch_kv_plan(a, static_cast<hipStream_t>(stream));
-    if (e != hipSuccess) return hip_fail(e, who);
-    return MOE_OK;
+    if (moe_status st = check_plan(L, n, t, max_pages, ldt,
+                                   length && grow && table && free_pages && free_n && length_out && free_n_out && starts &&
+                                       positions && slots && lacking,
+                                   int_aligned({length, grow, table, free_pages, free_n, length_out, free_n_out, starts,
+                                                positions, slots, lacking}),
+                                   who))
+        return st;
+    return kv_plan(length, grow, n, t, L, table, max_pages, ldt, free_pages, free_n, length_out, free_n_out, nullptr, starts,
+                   positions, slots, lacking, static_cast<hipStream_t>(stream), who);
+}
+
+moe_status moe_kv_plan_step(int32_t *length, const int32_t *grow, int32_t n, int32_t t, const moe_kv_layout *L,
+                            int32_t *table, int32_t max_pages, int64_t ldt, int32_t *free_pages, int32_t *free_n,
+                            int32_t *before, int32_t again, int32_t *starts, int32_t *positions, int32_t *slots,
+                            int32_t *lacking, void *stream) {
+    const char *who = "kv_plan_step";
+    if (moe_status st = check_plan(L, n, t, max_pages, ldt,
+                                   length && grow && table && free_pages && free_n && before && starts && positions &&
+                                       slots && lacking,
+                                   int_aligned({length, grow, table, free_pages, free_n, before, starts, positions, slots,
+                                                lacking}),
+                                   who))
+        return st;
+    const Rows rb = ints(before, (size_t)n + 1);
+    for (const Rows &x : {ints(length, n), ints(grow, n), ints(table, (size_t)(n - 1) * ldt + max_pages),
+                          ints(free_pages, L->pages), ints(free_n, 1), ints(starts, (size_t)n + 1), ints(positions, t),
+                          ints(slots, t), ints(lacking, 1)})
+        if (overlap(rb, x, 1)) return fail(MOE_ERR_INVALID, "%s: before overlaps another argument", who);
+    return kv_plan(again ? before : length, grow, n, t, L, table, max_pages, ldt, free_pages, again ? before + n : free_n,
+                   length, free_n, again ? nullptr : before, starts, positions, slots, lacking,
+                   static_cast<hipStream_t>(stream), who);
 }
 
 moe_status moe_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t x_type, int32_t t,
@@ -237,16 +278,38 @@ moe_status moe_attention_decode(const uint16_t *q, int64_t ldq, const int32_t *s
                                 int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
                                 int32_t max_pages, int64_t ldt, const int32_t *length, float scale, uint16_t *out,
                                 int64_t ldo, void *workspace, size_t workspace_bytes, void *stream) {
-    return attention(false, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, scale, out, ldo,
-                     workspace, workspace_bytes, static_cast<hipStream_t>(stream), "attention_decode");
+    return attention(false, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, nullptr, scale, out,
+                     ldo, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "attention_decode");
+}
+
+moe_status moe_attention_decode_step(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                     int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                     int32_t max_pages, int64_t ldt, const int32_t *length, const int32_t *before,
+                                     float scale, uint16_t *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    const char *who = "attention_decode_step";
+    if (!before) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
+    return attention(false, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, before, scale, out,
+                     ldo, workspace, workspace_bytes, static_cast<hipStream_t>(stream), who);
 }
 
 moe_status moe_attention_prefill(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
                                  int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
                                  int32_t max_pages, int64_t ldt, const int32_t *length, float scale, uint16_t *out,
                                  int64_t ldo, void *workspace, size_t workspace_bytes, void *stream) {
-    return attention(true, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, scale, out, ldo,
-                     workspace, workspace_bytes, static_cast<hipStream_t>(stream), "attention_prefill");
+    return attention(true, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, nullptr, scale, out,
+                     ldo, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "attention_prefill");
+}
+
+moe_status moe_attention_prefill_step(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
+                                      int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
+                                      int32_t max_pages, int64_t ldt, const int32_t *length, const int32_t *before,
+                                      float scale, uint16_t *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                      void *stream) {
+    const char *who = "attention_prefill_step";
+    if (!before) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
+    return attention(true, q, ldq, starts, t, n, heads_q, L, cache, table, max_pages, ldt, length, before, scale, out,
+                     ldo, workspace, workspace_bytes, static_cast<hipStream_t>(stream), who);
 }
 
 }  // extern "C"

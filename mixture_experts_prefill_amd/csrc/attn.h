@@ -16,10 +16,11 @@ struct KvCache {
     int pages, shift, heads, head, type;
 };
 
-// The fields are moe_kv_plan's arguments.
+// The fields are moe_kv_plan's arguments; keep: null, or where lengths and the
+// number of free pages are kept as they were [n + 1].
 struct KvPlanArgs {
     const int32_t *length, *grow, *free_n;
-    int32_t *table, *free_pages, *length_out, *free_n_out, *starts, *positions, *slots, *lacking;
+    int32_t *table, *free_pages, *length_out, *free_n_out, *starts, *positions, *slots, *lacking, *keep;
     int64_t ldt;
     int n, t, pages, shift, max_pages;
 };
@@ -50,6 +51,7 @@ struct AttentionArgs {
     const uint16_t *q;
     uint16_t *out;
     const int32_t *table, *length, *starts;  // starts: null if row s is sequence s's (decode)
+    const int32_t *before;                   // tokens before the rows; null: length less the rows
     int64_t ldq, ldo, ldt;
     int t, n, heads_q, max_tokens;
     // set by the launcher: tokens of a part at the least, and of a whole prompt

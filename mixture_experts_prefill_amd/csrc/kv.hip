@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(THREADS) k_kv_plan(KvPlanArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int s = s0 + i;
-        len[i] = s < n ? min(max(a.length[s], 0), limit) : 0;
+        len[i] = s < n ? a.length[s] : 0;
+        if (a.keep && s < n) a.keep[s] = len[i];
+        len[i] = min(max(len[i], 0), limit);
         const int g = s < n ? a.grow[s] : 0;
         asked += max(g, 0);
         rows[i] = min(max(g, 0), t);
@@ -90,7 +92,9 @@ __global__ void __launch_bounds__(THREADS) k_kv_plan(KvPlanArgs a) {
         ends += done[i] > 0;
         if (g < 0) rows[i] = -1;
     }
-    const int free_n = min(max(*a.free_n, 0), a.pages);
+    int free_n = *a.free_n;
+    if (a.keep && tid == 0) a.keep[n] = free_n;
+    free_n = min(max(free_n, 0), a.pages);
     if (tid == 0) left_out = 0;
     int r = wave_scan(own), b = wave_scan(back, kCap), d = wave_scan(ends);
     row_sums.put(r);
