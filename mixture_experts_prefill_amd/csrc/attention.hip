@@ -1168,8 +1168,7 @@ __global__ void __launch_bounds__(256) k_join_rows(AttentionArgs a) {
         if (lane < split) mine = a.stats[place(lane)];
         float top = mine.x;
         for (int i = lane + 64; i < split; i += 64) top = fmaxf(top, a.stats[place(i)].x);
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+        top = wave_max(top);
         float w = mine.y * part_weight(mine.x, top, cs), l = w;
         for (int i = lane + 64; i < split; i += 64) l += a.stats[place(i)].y * part_weight(a.stats[place(i)].x, top, cs);
         l = wave_sum(l);
