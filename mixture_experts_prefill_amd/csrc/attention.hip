@@ -204,9 +204,11 @@ __device__ __forceinline__ bool find_unit(const AttentionArgs &a, int v, int gro
             }
         }
         __syncthreads();
-        if (found.s < 0) return false;
-        u = found;
-        for (int w = 0; w < 4; ++w) u.cuts += wave_parts[w];
+        auto get = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+        if (get(found.s) < 0) return false;
+        u = Unit{get(found.s), get(found.len), get(found.rows), get(found.first), get(found.before), get(found.tile),
+                 get(found.split), get(found.part), get(found.slot),
+                 get(wave_parts[0] + wave_parts[1] + wave_parts[2] + wave_parts[3])};
     }
     // the tiles of a sequence run from its last, which have the most tokens; slots are in the order of the tiles
     u.slot += u.tile * u.split + u.part;
@@ -244,22 +246,84 @@ __device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int gro
 // 2^8, divided at the end only, may pass fp32 where the values do not, as may
 // the largest score times the scale (weights are then 0 or infinite, and their
 // sum too).  They run as if none of this occurred, and an output that then is
-// not finite is computed here, from the definition:
-//
-//   y = sum_j (w_j / l) v_j over the finite values, or the sum of those that are not
-//
-// 16 lanes a row, a token each: tokens j0 .. j1 - 1 of the sequence whose pages
-// are `pages`, key head h, query row q.  m and l are the row's maximum and sum;
-// columns 4 (lane % 16 + 16 i) .. + 3 are y[i].  Scores are scaled after the
-// largest is taken off.  No step of the fast path: an
-// output takes as long as the row's products without the matrix core, three times.
+// not finite is put right by the wave that wrote it: a look through the values
+// for those that are not finite, and if it was none of them, the row by its
+// definition.  A call whose outputs are finite pays for the look at them (1% of
+// most; of heads of 256 up to 3%).  One infinite value: 4096 rows 150 -> 640 us,
+// decode of 32 x 16000 tokens 360 -> 460; all values 3e38: 44 ms and 6.5 ms.
+
+// Whether any bf16 of a cell is an infinity or NaN.
+__device__ __forceinline__ bool not_finite(u32x4 w) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+    return bad;
+}
+
+// Whether any of a cell's e4m3 values is NaN, or may pass fp32 by its scale.
+__device__ __forceinline__ bool not_finite_e4m3(u32x4 w, u32x4 scale) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bad = bad || (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);   // a code of 0x7f
+        bad = bad || (scale[i] & ((scale[i] & 0x7f7f7f7fu) + 0x09090909u) & 0x80808080u);  // a scale byte above 246
+    }
+    return bad;
+}
+__device__ __forceinline__ uint32_t word_of(u32x4 w, int i) { return i < 2 ? i < 1 ? w.x : w.y : i < 3 ? w.z : w.w; }
+
+// Adds to wild[i] what of column lane + 64 i is not finite in tokens j .. end - 1
+// of the sequence whose pages are `pages`.
 template <int CT, int D>
-__device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const int32_t *pages, int h, const uint16_t *q,
-                                                  int j0, int j1, float cs, float &m, float &l, f32x4 (&y)[D / 64]) {
+__device__ __forceinline__ void add_not_finite(const KvCache &c, const int32_t *pages, int h, int j, int end,
+                                               float (&wild)[D / 64]) {
+    constexpr bool E4M3 = CT == MOE_E4M3;
+    constexpr int SIZE = E4M3 ? 1 : 2, C = 16 / SIZE, AT_ONCE = 256 / D;  // tokens a cell, cells of a column
+    const int lane = threadIdx.x & 63, page_mask = (1 << c.shift) - 1;
+#pragma unroll 1
+    for (int jb = j & ~(C - 1); jb < end; jb += C * AT_ONCE) {
+        u32x4 w[AT_ONCE][D / 64], sw[AT_ONCE];
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x) {
+            const int jx = jb + x * C, p = jx < end ? pages[jx >> c.shift] : -1;
+            const bool there = (unsigned)p < (unsigned)c.pages;
+            const size_t at = (((size_t)(there ? p : 0) * c.heads + h) << c.shift) + (jx & page_mask);
+            sw[x] = (u32x4){0, 0, 0, 0};
+            if (E4M3 && there) sw[x] = *reinterpret_cast<const u32x4 *>(c.vs + at);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                w[x][i] = (u32x4){0, 0, 0, 0};
+                if (there) w[x][i] = *reinterpret_cast<const u32x4 *>(c.v + at * (D * SIZE) + (lane + 64 * i) * 16);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                if (!(E4M3 ? not_finite_e4m3(w[x][i], sw[x]) : not_finite(w[x][i]))) continue;
+#pragma unroll 1
+                for (int e = max(j - jb - x * C, 0); e < min(end - jb - x * C, C); ++e) {
+                    const int word = e * SIZE / 4, shift = e * SIZE % 4 * 8;
+                    const uint32_t bits = word_of(w[x][i], word) >> shift;
+                    const float v = E4M3 ? __builtin_amdgcn_cvt_f32_fp8(bits, 0) * scale_of(word_of(sw[x], word) >> shift, 0) : bf16_lo(bits);
+                    if (!q8::finite(v)) wild[i] += v;
+                }
+            }
+    }
+}
+
+// The row of query q over the finite values of tokens j0 .. j1 - 1,
+//
+//   y = sum_j (w_j / l) v_j,  w_j = exp(scale (s_j - m)),
+//
+// a token a lane; columns lane + 64 i are y[i].
+template <int CT, int D>
+__device__ __forceinline__ void row_by_definition(const KvCache &c, const int32_t *pages, int h, const uint16_t *q, int j0,
+                                                  int j1, float cs, float &m, float &l, float (&y)[D / 64]) {
     constexpr bool E4M3 = CT == MOE_E4M3;
     constexpr int SIZE = E4M3 ? 1 : 2, C = 16 / SIZE;  // values a cell
-    const KvCache &c = a.c;
-    const int lane = threadIdx.x & 63, mine = lane & 15, page_mask = (1 << c.shift) - 1;
+    const int lane = threadIdx.x & 63, page_mask = (1 << c.shift) - 1;
     auto page_of = [&](int j) {
         const int p = j < j1 ? pages[j >> c.shift] : -1;
         return (unsigned)p < (unsigned)c.pages ? p : -1;
@@ -271,7 +335,7 @@ __device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const 
         const int in = j & page_mask;
         const uint8_t *k = c.k + (blk + (in & ~15)) * (D * SIZE) + (in & 15) * 16;
         float s = 0.0f;
-#pragma unroll 1
+#pragma unroll 4
         for (int d = 0; d < D; d += C) {
             const u32x4 kw = *reinterpret_cast<const u32x4 *>(k + d / C * 256);
 #pragma unroll
@@ -300,43 +364,65 @@ __device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const 
     };
     m = minus_inf();
 #pragma unroll 1
-    for (int j = j0 + mine; j < j1; j += 16) m = fmaxf(m, score(j, page_of(j)));
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    for (int j = j0 + lane; j < j1; j += 64) m = fmaxf(m, score(j, page_of(j)));
+    m = wave_max(m);
     const float top = m == minus_inf() ? 0.0f : m;
     l = 0.0f;
 #pragma unroll 1
-    for (int j = j0 + mine; j < j1; j += 16) l += __builtin_amdgcn_exp2f((score(j, page_of(j)) - top) * cs);
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    for (int j = j0 + lane; j < j1; j += 64) l += __builtin_amdgcn_exp2f((score(j, page_of(j)) - top) * cs);
+    l = wave_sum(l);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    f32x4 wild[D / 64];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) y[i] = wild[i] = (f32x4){0, 0, 0, 0};
+    for (int i = 0; i < D / 64; ++i) y[i] = 0.0f;
 #pragma unroll 1
-    for (int jb = j0; jb < j1; jb += 16) {
-        const int p = page_of(jb + mine);
-        const float w = __builtin_amdgcn_exp2f((score(jb + mine, p) - top) * cs) * inv;
-#pragma unroll 1
-        for (int x = 0; x < 16; ++x) {
-            const int px = __shfl(p, (lane & 48) + x, 64);
-            const float wx = __shfl(w, (lane & 48) + x, 64);
+    for (int jb = j0; jb < j1; jb += 64) {
+        const int p = page_of(jb + lane);
+        const float w = __builtin_amdgcn_exp2f((score(jb + lane, p) - top) * cs) * inv;
+#pragma unroll 4
+        for (int x = 0; x < 64; ++x) {
+            const int px = __builtin_amdgcn_readlane(p, x);
+            const float wx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), x));
             if (px < 0) continue;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = value(jb + x, px, 4 * (mine + 16 * i) + e);
-                    if (q8::finite(v)) y[i][e] = __builtin_fmaf(wx, v, y[i][e]);
-                    else wild[i][e] += v;
-                }
+            for (int i = 0; i < D / 64; ++i) {
+                const float v = value(jb + x, px, lane + 64 * i);
+                y[i] = __builtin_fmaf(q8::finite(v) ? wx : 0.0f * wx, q8::finite(v) ? v : 0.0f, y[i]);  // (NaN weights stay)
+            }
         }
     }
+}
+
+// The kernel's arguments, read anew, so that what only outputs that are not
+// finite need is not held in registers along a kernel's loop (k_prefill: 21 scalar
+// registers spilled there, 1000 rows of heads of 256 39.0 -> 40.7 us; so 39.5).
+__device__ __forceinline__ const AttentionArgs &args_again() {
+    const AttentionArgs *args = reinterpret_cast<const AttentionArgs *>((uintptr_t)__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(args));
+    return *args;
+}
+
+// Whether a row whose sum of weights is l can be put right: where no score can
+// pass fp32 by the scale, a sum that is not finite is that of a score, and the
+// row is NaN already.
+__device__ __forceinline__ bool sound(float l) { return l > 0.0f && l < __builtin_inff(); }
+__device__ __forceinline__ bool lost(float l, float cs) { return !sound(l) && cs <= 1.0f; }
+
+// What of a row's outputs is put right: column lane + 64 i, where wrong(i), by
+// put(i, output); wild: what add_not_finite found for the row's tokens; l: the
+// fast path's sum.  Returns whether m and l are new.
+template <int CT, int D, class Wrong, class Put>
+__device__ __forceinline__ bool put_right(const KvCache &c, const int32_t *pages, int h, const uint16_t *q, int j0, int j1,
+                                          float cs, const float (&wild)[D / 64], float &m, float &l, Wrong wrong, Put put) {
+    bool more = !sound(l);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) more = more || (wrong(i) && wild[i] == 0.0f);
+    more = __any(more);
+    float y[D / 64];
+    if (more) row_by_definition<CT, D>(c, pages, h, q, j0, j1, cs, m, l, y);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            y[i][e] = l == 0.0f ? 0.0f : wild[i][e] != 0.0f ? wild[i][e] + 0.0f * l : y[i][e];  // (l: NaN if a score is)
+        if (wrong(i)) put(i, more && l == 0.0f ? 0.0f : wild[i] != 0.0f ? wild[i] + 0.0f * l : y[i]);  // (l: NaN if a score is)
+    return more;
 }
 
 // ------------------------------------------------------------------ one row a sequence
@@ -351,7 +437,7 @@ __device__ __forceinline__ void row_by_definition(const AttentionArgs &a, const 
 // operands in registers while one is used made no difference: eight or twelve
 // waves a CU have enough on the way.)
 template <int CT, int D, bool SMALL>
-__global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16 ? 2 : 1) k_decode(AttentionArgs a) {
+__global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : CT == MOE_BF16 ? 2 : 1) k_decode(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;
     constexpr int SIZE = E4M3 ? 1 : 2, TK = E4M3 ? 64 : 32, NB = TK / 16, KEYS = TK / 4;  // KEYS: of one lane
     constexpr int KL = E4M3 ? D / 64 : D / 32, VL = D / 16;                               // loads a block of 16, a tile
@@ -515,13 +601,16 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
     }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (g == 0) {
+    int quarter = lane;  // g again, which is then not held along the loop (spilled with heads of 256: 486 -> 492 us)
+    asm volatile("" : "+v"(quarter));
+    quarter >>= 4;
+    if (quarter == 0) {
         red_m[wave][m] = mx;
         red_l[wave][m] = l;
     }
     // [wave][row m][D], the float4 of columns 16 i + 4 g at place (4 i + g) ^ m: no bank twice
 #pragma unroll
-    for (int i = 0; i < VL; ++i) *reinterpret_cast<f32x4 *>(&red[(wave * 16 + m) * D + ((4 * i + g) ^ m) * 4]) = o[i];
+    for (int i = 0; i < VL; ++i) *reinterpret_cast<f32x4 *>(&red[(wave * 16 + m) * D + ((4 * i + quarter) ^ m) * 4]) = o[i];
     __syncthreads();
     bool wild = false;
     auto part_at = [&](int r) { return ((size_t)u.slot * HT + ht) * a.part_rows + r; };
@@ -551,28 +640,32 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : D == 256 && CT == MOE_BF16
     }
     if (__builtin_expect(!__any(wild), 1)) return;
     __threadfence_block();  // other lanes wrote what is read below
-    // the rows that this wave wrote above, four at a time: 256 / D of each turn of the loop
+    const AttentionArgs &b = args_again();
+    const int32_t *pages = b.table + u.s * b.ldt;
+    const int j0 = t0 * TK, j1 = min(t1 * TK, u.len);
+    float v_wild[D / 64] = {};
+    add_not_finite<CT, D>(b.c, pages, h, j0, j1, v_wild);
+    // the rows that this wave wrote above: 256 / D of each turn of the loop
     constexpr int EACH = 256 / D;
-    const int r = wave * EACH + g % EACH + g / EACH * (4 * EACH);
-    if (r >= nq) return;
-    float m_r, l_r;
-    f32x4 y[D / 64];
-    row_by_definition<CT, D>(a, row, h, a.q + u.first * a.ldq + (size_t)(h * G + q0 + r) * D, t0 * TK, min(t1 * TK, u.len),
-                             cs, m_r, l_r, y);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const int col = m + 16 * i;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int r = wave * EACH + i % EACH + i / EACH * (4 * EACH);
+        if (r >= nq) continue;
+        float top = red_m[0][r], ls = 0.0f;
+        for (int w = 1; w < 4; ++w) top = fmaxf(top, red_m[w][r]);
+        for (int w = 0; w < 4; ++w)
+            ls += red_m[w][r] == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f((red_m[w][r] - top) * cs) * red_l[w][r];
+        if (lost(ls, cs)) continue;
+        const uint16_t *q = b.q + u.first * b.ldq + (size_t)(h * G + q0 + r) * D;
         if (u.split == 1) {
-            uint16_t *to = out_at(r, col);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if ((to[e] & 0x7f80) == 0x7f80) to[e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
+            uint16_t *to = out_at(r, 0) + lane;
+            put_right<CT, D>(b.c, pages, h, q, j0, j1, cs, v_wild, top, ls, [&](int i) { return (to[64 * i] & 0x7f80) == 0x7f80; },
+                             [&](int i, float y) { to[64 * i] = (uint16_t)pk_bf16(y, 0.0f); });
         } else {
-            float *to = a.part + part_at(r) * D + col * 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!q8::finite(to[e])) to[e] = y[i][e];
-            if (col == 0) a.stats[part_at(r)] = make_float2(m_r, l_r);
+            float *to = b.part + part_at(r) * D + lane;
+            if (put_right<CT, D>(b.c, pages, h, q, j0, j1, cs, v_wild, top, ls, [&](int i) { return !q8::finite(to[64 * i]); },
+                                 [&](int i, float y) { to[64 * i] = y; }) && lane == 0)
+                b.stats[part_at(r)] = make_float2(top, ls);
         }
     }
 }
@@ -592,66 +685,48 @@ __device__ __forceinline__ void dma16(uint32_t to, const void *from, uint32_t la
                  : : "s"(to - offset), "v"(lane_offset), "s"(from), "i"(offset) : "memory", "m0");
 }
 
-// Whether any bf16 of a cell is an infinity or NaN.
-__device__ __forceinline__ bool not_finite(u32x4 w) {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
-}
-
 // What rows that are computed again need of their unit.
 struct Again {
     int s, len, first, slot;          // the sequence, its tokens, its first row, the unit's partial result (-1: none)
     int x0, pairs, before, j0, j1;    // the tile's first pair, the sequence's pairs, its first row's position, the unit's tokens
 };
-// The outputs of the wave's 32 pairs that are not finite, by definition, in
-// the place of what k_prefill has written.  All that is known of the launch is read
-// anew, so that none of it has to be held in registers along k_prefill's loop
-// (21 scalar registers spilled there, 1000 rows of heads of 256 39.0 -> 40.7 us; so 39.4).
+// The outputs of the wave's 32 pairs that are not finite, put right in the place
+// that k_prefill has written; m, l: pair lane % 32's largest score and sum.
 template <int CT, int D>
-__device__ __forceinline__ void rows_again(const Again &n) {
-    const AttentionArgs *args = reinterpret_cast<const AttentionArgs *>((uintptr_t)__builtin_amdgcn_kernarg_segment_ptr());
-    asm volatile("" : "+s"(args));
-    const AttentionArgs &a = *args;
+__device__ __forceinline__ void rows_again(const Again &n, float m, float l) {
+    const AttentionArgs &a = args_again();
     __threadfence_block();  // other lanes wrote what is read below
-    const int H = a.c.heads, G = a.heads_q / H, h = blockIdx.x % H, lane = threadIdx.x & 63, mine = lane % 16;
+    const int H = a.c.heads, G = a.heads_q / H, h = blockIdx.x % H, lane = threadIdx.x & 63;
     const int32_t *pages = a.table + n.s * a.ldt;
     const float cs = a.scale * kLog2e;
     const int x0 = n.x0 + (threadIdx.x >> 6) * 32, rows = min(32, n.pairs - x0);
     const size_t block = ((size_t)n.slot * H + h) * (a.part_rows / 32) + (threadIdx.x >> 6);
+    float wild[D / 64] = {};
+    int seen = n.j0;  // wild is of the tokens before this one: later pairs read as many or more
 #pragma unroll 1
-    for (int r = lane / 16; r < rows; r += 4) {  // 16 lanes a pair
-        const int token = (x0 + r) / G, hq = h * G + (x0 + r) % G;
-        uint16_t *out = a.out + (size_t)(n.first + token) * a.ldo + (size_t)hq * D + 4 * mine;
-        // (by_tile: columns 32 i + 8 j + 4 k .. + 3 of a row stand at (4 i + j) * 64 + 32 k + row)
-        const size_t at = a.by_tile ? (block * (D / 8) + mine / 2) * 64 + mine % 2 * 32 + r : (block * 32 + r) * (D / 4) + mine;
-        float *part = a.part + at * 4;
-        const int step = a.by_tile ? 8 * 64 * 4 : 64;  // 64 columns further
-        auto wild = [&](int i, int e) {
-            return n.slot < 0 ? (out[64 * i + e] & 0x7f80) == 0x7f80 : !q8::finite(part[i * step + e]);
-        };
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) any = any || wild(i, e);
-        if (!(__ballot(any) >> (lane & 48) & 0xffff)) continue;
-        float m, l;
-        f32x4 y[D / 64];
-        const int pos = n.before + token;
-        row_by_definition<CT, D>(a, pages, h, a.q + (size_t)(n.first + token) * a.ldq + (size_t)hq * D, n.j0,
-                                 pos < n.len ? min(n.j1, pos + 1) : n.j0, cs, m, l, y);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (!wild(i, e)) continue;
-                if (n.slot < 0) out[64 * i + e] = (uint16_t)pk_bf16(y[i][e], 0.0f);
-                else part[i * step + e] = y[i][e];
-            }
-        if (n.slot >= 0 && mine == 0) a.stats[block * 32 + r] = make_float2(m, l);
+    for (int r = 0; r < rows; ++r) {
+        const int token = (x0 + r) / G, hq = h * G + (x0 + r) % G, pos = n.before + token;
+        if (pos >= n.len) break;  // no slot, nor has any pair after it
+        const int end = min(n.j1, pos + 1);
+        float m_r = __shfl(m, r, 64), l_r = __shfl(l, r, 64);
+        if (end <= n.j0 || lost(l_r, cs)) continue;
+        if (end > seen) add_not_finite<CT, D>(a.c, pages, h, seen, end, wild);
+        seen = max(seen, end);
+        const uint16_t *q = a.q + (size_t)(n.first + token) * a.ldq + (size_t)hq * D;
+        if (n.slot < 0) {
+            uint16_t *to = a.out + (size_t)(n.first + token) * a.ldo + (size_t)hq * D + lane;
+            put_right<CT, D>(a.c, pages, h, q, n.j0, end, cs, wild, m_r, l_r,
+                             [&](int i) { return (to[64 * i] & 0x7f80) == 0x7f80; },
+                             [&](int i, float y) { to[64 * i] = (uint16_t)pk_bf16(y, 0.0f); });
+        } else {
+            // (by_tile: columns 32 i + 8 j + 4 k .. + 3 of a row stand at (4 i + j) * 64 + 32 k + row)
+            float *to = a.part + (a.by_tile ? ((block * (D / 8) + lane / 8) * 64 + lane / 4 % 2 * 32 + r) * 4 + lane % 4
+                                            : (block * 32 + r) * D + lane);
+            const int step = a.by_tile ? 8 * 64 * 4 : 64;  // 64 columns further
+            if (put_right<CT, D>(a.c, pages, h, q, n.j0, end, cs, wild, m_r, l_r, [&](int i) { return !q8::finite(to[i * step]); },
+                                 [&](int i, float y) { to[i * step] = y; }) && lane == 0)
+                a.stats[block * 32 + r] = make_float2(m_r, l_r);
+        }
     }
 }
 
@@ -1086,7 +1161,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
                     (f32x4){o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]};
     }
     if (__builtin_expect(!__any(live && (wild.x + wild.y) + (wild.z + wild.w) != 0.0f), 1)) return;
-    rows_again<CT, D>(again);
+    rows_again<CT, D>(again, mx, l);
 }
 
 // ------------------------------------------------------------------ joining

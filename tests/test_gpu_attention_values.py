@@ -191,3 +191,70 @@ def test_scores_beyond_fp32(mep, n, scale, single):
         mep.moe_attention_prefill(q.cuda(), base.ints([0, rows]).cuda(), b.layout, cache, table, length, scale, out, ws)
     want = b.values(0)[1][best].view(1, head).expand(rows * hq, head)
     assert torch.equal(out.double().cpu().view(rows * hq, head), want)
+
+
+def overflowing(mep, n, head, hq, rows, largest, gen_seed=0):
+    """Scores of one head that are twice those of the other, of which token `best` has the largest."""
+    b = base.Batch(mep, [n], 1, head, 16, BF16, seed=gen_seed)
+    k = torch.zeros(n, 1, head)
+    k[:, 0, 0] = largest - torch.randint(1, 9, (n,), generator=b.gen).float() * 0.5
+    best = (n - rows) // 2
+    k[best, 0, 0] = largest
+    b.cache.write("k", b.slots[0], k.to(BF16))
+    q = torch.zeros(rows, hq * head, dtype=BF16)
+    q[:, 0], q[:, head] = 1.0, 2.0
+    return b, q, best
+
+
+def attend(mep, b, q, hq, scale, single):
+    rows = q.shape[0]
+    cache, table, length = b.on_gpu()
+    out = torch.empty(rows, hq * b.head, dtype=BF16, device="cuda")
+    ws = base.workspace(mep, rows, 1, hq, b.layout)
+    if single:
+        mep.moe_attention_decode(q.cuda(), b.layout, cache, table, length, scale, out, ws)
+    else:
+        mep.moe_attention_prefill(q.cuda(), base.ints([0, rows]).cuda(), b.layout, cache, table, length, scale, out, ws)
+    return out.double().cpu().view(rows * hq, b.head)
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("n", [1, 50, 700, 5000])
+def test_negative_scores_beyond_fp32(mep, n, single):
+    """The largest one is below -2^128 too."""
+    rows = 1 if single else min(n, 30)
+    b, q, best = overflowing(mep, n, 64, 2, rows, -1.5)
+    want = b.values(0)[1][best].view(1, 64).expand(rows * 2, 64)
+    assert torch.equal(attend(mep, b, q, 2, 2.0 ** 127, single), want)
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("n", [2, 50, 700, 5000])
+def test_infinite_values_beside_scores_beyond_fp32(mep, n, single):
+    rows = 1 if single else min(n - 1, 30)
+    b, q, best = overflowing(mep, n, 64, 2, rows, 3.0)
+    set_value(b, 0, best, 9, torch.inf)
+    set_value(b, 0, (best + 1) % n, 50, -torch.inf)               # of no weight
+    want = b.values(0)[1][best].view(1, 1, 64).expand(rows, 2, 64).clone()
+    reads = torch.tensor([n - rows + i >= (best + 1) % n for i in range(rows)])
+    want[reads, :, 50] = -torch.inf
+    assert torch.equal(attend(mep, b, q, 2, 2.0 ** 127, single), want.view(rows * 2, 64))
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("scale", [0.1, 2.0, 2.0 ** 100])
+@pytest.mark.parametrize("n,tok,v", [(70, 40, torch.nan), (3000, 2980, torch.nan), (3000, 100, torch.inf)])
+def test_scores_that_are_not_finite(mep, n, tok, v, scale, single):
+    """A key of NaN, or a score of plus infinity, leaves its readers nothing but NaN, beside an infinite value too."""
+    rows, hq, head = 1 if single else 60, 2, 128
+    b = base.Batch(mep, [n], 1, head, 16, BF16)
+    b.cache.section("k")[b.cache.index("k", [b.slots[0][tok]])[0, 0, 3]] = v
+    set_value(b, 0, 5, 17, torch.inf)
+    q = b.queries(rows, hq)
+    q[:, 3], q[:, head + 3] = 1.0, 0.5
+    got = attend(mep, b, q, hq, scale, single).view(rows, hq, head)
+    for i in range(rows):
+        if n - rows + i >= tok:
+            assert bool(torch.isnan(got[i]).all()), i
+        else:
+            assert bool((got[i, :, 17] == torch.inf).all()) and int((~torch.isfinite(got[i])).sum()) == hq, i
