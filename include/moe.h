@@ -727,8 +727,8 @@ moe_status moe_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv,
 /*
  * Bytes of the workspace of moe_attention_decode and moe_attention_prefill
  * for t rows of n sequences and heads_q query heads on this cache.  It needs
- * no initial value; calls that may run
- * at the same time (on other streams, in other graphs) need one each.
+ * no initial value; calls that may run at the same time (on other streams, in
+ * other graphs) need one each.
  * Returns 0 for invalid arguments.  Host only.
  */
 size_t moe_attention_workspace_bytes(int32_t t, int32_t n, int32_t heads_q, const moe_kv_layout *L);
@@ -775,8 +775,11 @@ moe_status moe_attention_decode(const uint16_t *q, int64_t ldq, const int32_t *s
  *   q       bf16 [t][heads_q * head], row stride ldq;  out bf16, row stride ldo
  *   starts  [n + 1], ascending, 0 .. t;  the rest as for moe_attention_decode
  * The weights p_j are rounded to bf16 before they are summed and meet v;
- * scores, softmax and sums are fp32.  Requires 1 <= t <=
- * MOE_MAX_ROWS and a workspace of moe_attention_workspace_bytes(t, n, heads_q, L).
+ * scores, softmax and sums are fp32.  How sequences that are cut are joined
+ * goes by t, which should not be many times the rows that starts hold (1 row
+ * of 32 heads after 8000 tokens: 14 us with t up to 128, 23.5 with more).
+ * Requires 1 <= t <= MOE_MAX_ROWS and a workspace of
+ * moe_attention_workspace_bytes(t, n, heads_q, L).
  */
 moe_status moe_attention_prefill(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
                                  int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,

@@ -14,7 +14,8 @@
 // 16) neighbouring tokens that its V operand holds, a cell of the cache.
 //
 // m grows only when a score exceeds it by more than 2^8 in weight: weights up
-// to 256 cost no precision, and o is rescaled once or twice a sequence.
+// to 256 cost no precision, and o is rescaled that often only (once or twice a
+// sequence where scores do not rise along it).
 #include <hip/hip_runtime.h>
 
 #include "attn.h"
@@ -40,8 +41,8 @@ constexpr float kMostSlack = 1e38f;    // finite, so that the first score sets t
 // How many tokens a part has: as many as make `few` units of all tiles, but
 // from `least` to `enough`; and at least as many as make `many` units.  The
 // chip holds 512 workgroups at a time (256 of heads of 256).  Decode: with
-// {512, 128, 1024, 2048} one sequence of 1000 tokens takes 7.7 us and one of
-// 32000 36 us (2048 units of 128 and more: 10.3 and 45), 32 of 16000 359 (1024:
+// {512, 128, 1024, 2048} one sequence of 1000 tokens takes 7.6 us and one of
+// 32000 35 us (2048 units of 128 and more: 10.3 and 45), 32 of 16000 359 (1024:
 // 363).  Prefill: more than 512 units were slower wherever tiles were cut.
 struct Cut {
     int few, least, enough, many;
@@ -61,8 +62,8 @@ constexpr int kUncut = 512;
 // tokens 22.1 -> 29.6, so not there.
 constexpr int kLeastTiles = 512, kLeastWhole = 2048, kWholeTiles = 200;
 // At most so many (row, query head)s are joined by a workgroup each, more by
-// tiles: 64 rows of 32 heads after 4 x 2000 tokens 15.6 (by tiles 19.6), 1 row
-// after 8000 14.8 (42.6); 1000 rows after 4 x 1000 26.6 (23.3), 1024 after
+// tiles: 64 rows of 32 heads after 4 x 2000 tokens 16.2 (by tiles 19.6), 1 row
+// after 8000 14.1 (23.5); 1000 rows after 4 x 1000 26.6 (23.6), 1024 after
 // 16 x 1000, e4m3, 49.9 (42.6).
 constexpr int kWideItems = 4096;
 
@@ -124,7 +125,9 @@ __device__ __forceinline__ Seq seq_of(const AttentionArgs &a, int s, int group) 
 template <bool PREFILL>
 __device__ __forceinline__ int part_tokens(float work, int heads) {
     constexpr Cut cut = PREFILL ? kPrefillCut : kDecodeCut;
-    // (fp32 is off by 2^-20 of it at most, by which no count of units can pass the next whole number)
+    // (In fp32 `work` is off by less than 2^-19: up to 16 sums a lane, 6 over the lanes, 4 over the waves, and the
+    // products.  The units of a head are then at most tiles + many / heads (1 + 2^-19), and the excess is below 1 /
+    // heads: the whole number that the grid and the workspace are made for is not passed.)
     work *= heads;
     const float few = fminf(fmaxf(work / cut.few, (float)cut.least), (float)cut.enough);
     return (int)fminf(ceilf(fmaxf(work / cut.many, few)), 1073741824.0f);
@@ -433,9 +436,10 @@ __device__ __forceinline__ bool put_right(const KvCache &c, const int32_t *pages
 // operands, and add up their outputs in LDS at the end.  The weights enter the
 // second product as two bf16 terms, p = hi + lo, which costs nothing where
 // memory is the bound.  Bound by memory: 32 sequences of 16000 tokens, 32 / 8
-// heads of 128, 359 us, 5.7 TB/s, 96% of a streaming read.  (The next tile's
-// operands in registers while one is used made no difference: eight or twelve
-// waves a CU have enough on the way.)
+// heads of 128, 360 us, 5.7 TB/s, 96% of a streaming read.  (The next tile's
+// operands in registers while one is used made no difference there: twelve
+// waves a CU have enough on the way.  Heads of 256 leave room for eight, in
+// e4m3 for four: 32 x 8000 tokens, 16 / 8 heads, 338 and 200 us, 5.75 and 4.9 TB/s.)
 template <int CT, int D, bool SMALL>
 __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : CT == MOE_BF16 ? 2 : 1) k_decode(AttentionArgs a) {
     constexpr bool E4M3 = CT == MOE_E4M3;
@@ -1330,8 +1334,7 @@ hipError_t launch_type(const AttentionArgs &a, hipStream_t s) {
     const int G = a.heads_q / a.c.heads;
     const bool prefill = a.prefill;
     const int HT = prefill ? a.c.heads : a.c.heads * ((G + kDecodeRows - 1) / kDecodeRows);
-    // no more units than this: the cuts that the target allows, and a unit a tile
-    const int tiles = prefill ? a.t * G / kPrefillRows + a.n : a.n;
+    const int tiles = prefill ? a.t * G / kPrefillRows + a.n : a.n;  // of a head, or fewer
     const Cut cut = prefill ? kPrefillCut : kDecodeCut;
     // no more units of a head than the cuts make, and a unit a tile; nor than the tables' tokens allow
     const int64_t most = (int64_t)tiles * ((a.max_tokens + a.least - 1) / a.least);

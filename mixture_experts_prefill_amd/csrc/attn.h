@@ -41,9 +41,10 @@ hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 // Work units of the attention kernels.  A tile is the rows that one workgroup
 // takes at a time: up to kDecodeRows query heads of one key head (decode), or
 // kPrefillRows (row, query head) pairs of one key head (prefill).  A
-// sequence's tiles are cut along its tokens into `split` units each, so that
-// all tiles together make about `target` units; tiles of more than one unit
-// leave partial results in the workspace, which a second launch joins.
+// sequence's tiles are cut along its tokens into `split` units each, of a
+// length that follows from the work of all tiles (Cut in attention.hip); tiles
+// of more than one unit leave partial results in the workspace, which a second
+// launch joins.
 constexpr int kDecodeRows = 16, kPrefillRows = 128;
 constexpr int kMaxHeadsQ = 1024;
 struct AttentionArgs {
