@@ -246,9 +246,8 @@ __device__ __forceinline__ bool take_unit(const AttentionArgs &a, int v, int gro
 // (two of unequal signs make NaN), however small the weight.  The matrix
 // products do not give that: 0 times infinity is NaN, and so is infinity
 // times a weight's two terms of unequal signs.  And their sums of weights up to
-// 2^8, divided at the end only, may pass fp32 where the values do not, as may
-// the largest score times the scale (weights are then 0 or infinite, and their
-// sum too).  They run as if none of this occurred, and an output that then is
+// 2^8, divided at the end only, may pass fp32 where the values do not, and
+// weights relative to a score far from 0 may all be 0 or infinite.  They run as if none of this occurred, and an output that then is
 // not finite is put right by the wave that wrote it: a look through the values
 // for those that are not finite, and if it was none of them, the row by its
 // definition.  A call whose outputs are finite pays for the look at them (1% of
@@ -404,11 +403,12 @@ __device__ __forceinline__ const AttentionArgs &args_again() {
     return *args;
 }
 
-// Whether a row whose sum of weights is l can be put right: where no score can
-// pass fp32 by the scale, a sum that is not finite is that of a score, and the
-// row is NaN already.
+// Weights are exp2(fma(s, cs, -mc)), mc the largest score's s cs rounded: of
+// scores beyond 2^28 or so its rounding alone may make all of them, and their
+// sum l, 0 or infinite.  Where cs is at most 1, l is NaN only if a score is NaN
+// or infinite, and with it the row is, rightly.
 __device__ __forceinline__ bool sound(float l) { return l > 0.0f && l < __builtin_inff(); }
-__device__ __forceinline__ bool lost(float l, float cs) { return !sound(l) && cs <= 1.0f; }
+__device__ __forceinline__ bool lost(float l, float cs) { return l != l && cs <= 1.0f; }
 
 // What of a row's outputs is put right: column lane + 64 i, where wrong(i), by
 // put(i, output); wild: what add_not_finite found for the row's tokens; l: the
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : CT == MOE_BF
             const float f = now == minus_inf() ? 1.0f : __builtin_amdgcn_exp2f((mx - now) * cs);
             mx = now;
             mc = now == minus_inf() ? 0.0f : now * cs;
-            l *= f;
+            l = f == 0.0f ? 0.0f : l * f;  // (l may be infinite, see put_right)
 #pragma unroll
             for (int i = 0; i < VL; ++i) o[i] *= f;
         }
@@ -657,8 +657,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : CT == MOE_BF
         if (r >= nq) continue;
         float top = red_m[0][r], ls = 0.0f;
         for (int w = 1; w < 4; ++w) top = fmaxf(top, red_m[w][r]);
-        for (int w = 0; w < 4; ++w)
-            ls += red_m[w][r] == minus_inf() ? 0.0f : __builtin_amdgcn_exp2f((red_m[w][r] - top) * cs) * red_l[w][r];
+        for (int w = 0; w < 4; ++w) {  // (a sum of scores of minus infinity and NaN only is NaN; infinite ones of no weight)
+            const float f = red_m[w][r] == minus_inf() ? 1.0f : __builtin_amdgcn_exp2f((red_m[w][r] - top) * cs);
+            ls += f == 0.0f ? 0.0f : f * red_l[w][r];
+        }
         if (lost(ls, cs)) continue;
         const uint16_t *q = b.q + u.first * b.ldq + (size_t)(h * G + q0 + r) * D;
         if (u.split == 1) {
@@ -920,7 +922,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_prefill(AttentionArgs
         const float f = now == minus_inf() ? 1.0f : __builtin_amdgcn_exp2f((mx - now) * cs);
         mx = now;
         mc = now == minus_inf() ? 0.0f : now * cs;
-        l *= f;
+        l = f == 0.0f ? 0.0f : l * f;  // (l may be infinite, see put_right)
 #pragma unroll
         for (int i = 0; i < ND; ++i) o[i] *= f;
     };

@@ -258,3 +258,20 @@ def test_scores_that_are_not_finite(mep, n, tok, v, scale, single):
             assert bool(torch.isnan(got[i]).all()), i
         else:
             assert bool((got[i, :, 17] == torch.inf).all()) and int((~torch.isfinite(got[i])).sum()) == hq, i
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("largest", [3.0, -1.5])
+@pytest.mark.parametrize("far", [2.0 ** 28, 2.0 ** 36, 2.0 ** 60])
+@pytest.mark.parametrize("n", [1, 50, 700, 5000])
+def test_far_scores(mep, n, far, largest, single):
+    """Scores in fp32 whose rounding alone is many powers of two in weight: the largest one's token is all there is.
+    They rise along the sequence, so that the sum is taken relative to one far score after the other."""
+    rows = 1 if single else min(n, 30)
+    b, q, best = overflowing(mep, n, 64, 2, rows, largest)
+    k = b.values(0)[0]
+    k[:best, 0, 0] = k[:best, 0, 0].sort().values
+    b.cache.write("k", b.slots[0], k.to(BF16))
+    q = (q.float() * far).to(BF16)
+    want = b.values(0)[1][best].view(1, 64).expand(rows * 2, 64)
+    assert torch.equal(attend(mep, b, q, 2, 0.1, single), want)
