@@ -756,9 +756,9 @@ size_t moe_attention_workspace_bytes(int32_t t, int32_t n, int32_t heads_q, cons
  * anything else.  Requires 1 <= t, n <= MOE_MAX_ROWS, heads_q a multiple of
  * heads up to 1024, max_pages * page <= 2^30; MOE_ERR_WORKSPACE for a
  * workspace smaller than moe_attention_workspace_bytes(t, n, heads_q, L).
- * Scores, softmax and sums are fp32 (a row that has a q . k beyond it is NaN;
- * scaled scores and sums of values may pass it); the result is bitwise the
- * same for the same arguments.
+ * Scores, softmax and sums are fp32: a q . k above its range or NaN makes its
+ * row NaN, one below it weighs nothing, and scaled scores and sums of values
+ * may pass it.  The result is bitwise the same for the same arguments.
  */
 moe_status moe_attention_decode(const uint16_t *q, int64_t ldq, const int32_t *starts, int32_t t, int32_t n,
                                 int32_t heads_q, const moe_kv_layout *L, const void *cache, const int32_t *table,
